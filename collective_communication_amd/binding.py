@@ -35,8 +35,12 @@ HC_OP_COMPRESS_SCOPED = 5
 HC_OP_COMPRESS_ENTROPY = 6
 HC_OP_COMPRESS_STAGED = 7
 HC_OP_ALLREDUCE_F32_CARRY = 8
+HC_NORM_L2 = 0
+HC_NORM_INF = 1
 HC_BLOCK_ELEMS = 16384
 HC_MAX_RANKS = 64
+HC_MAX_TOPK = 64
+HC_MAX_EXPERTS = 1024
 
 EXPORTED = [
     "hc_allreduce", "hc_reduce_scatter", "hc_all_gather", "hc_compress_bound_bf16",
@@ -46,6 +50,10 @@ EXPORTED = [
     "hc_compress_bf16_scoped", "hc_compress_bf16_entropy", "hc_decompress_bf16_entropy",
     "hc_compress_bf16_staged", "hc_allreduce_bf16_f32carry", "hc_compress_bf16_noalloc", "hc_cu_census",
     "hc_stream_create_cu_range", "hc_copy_engine_available",
+    "hc_grad_norm_workspace_bytes", "hc_grad_norm", "hc_clip_grads", "hc_clip_grad_norm", "hc_embedding",
+    "hc_embedding_grad_workspace_bytes", "hc_embedding_grad", "hc_expert_rows_bound",
+    "hc_expert_sort_workspace_bytes", "hc_expert_sort", "hc_expert_dispatch", "hc_expert_combine",
+    "hc_expert_combine_grad",
 ]
 
 
@@ -65,6 +73,13 @@ class hc_task_t(ctypes.Structure):
     _fields_ = [("src", ctypes.c_int32), ("dst", ctypes.c_int32), ("step", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("op", ctypes.c_int32), ("slice", ctypes.c_int32),
                 ("off", ctypes.c_uint64), ("len", ctypes.c_uint64)]
+
+
+class hc_expert_plan_t(ctypes.Structure):
+    _fields_ = [("ntokens", ctypes.c_size_t), ("k", ctypes.c_int32), ("nexperts", ctypes.c_int32),
+                ("row_align", ctypes.c_int32), ("rows", ctypes.c_size_t), ("row_of_slot", ctypes.c_void_p),
+                ("slot_of_row", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
+                ("expert_counts", ctypes.c_void_p)]
 
 
 _lib = None
@@ -106,6 +121,24 @@ def load(path: str = LIB_PATH):
     L.hc_chunk_elems.argtypes = [S, ctypes.c_double, S]
     L.hc_chunk_elems.restype = S
     L.hc_ring_tasks.argtypes = [I, S, S, ctypes.POINTER(hc_task_t), S]
+    F, I64 = ctypes.c_float, ctypes.c_int64
+    PS, PI, PE = ctypes.POINTER(S), ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(hc_expert_plan_t)
+    L.hc_grad_norm_workspace_bytes.argtypes = [S]
+    L.hc_grad_norm.argtypes = [PP, PS, PI, S, I, P, P, S, P]
+    L.hc_clip_grads.argtypes = [PP, PP, PS, PI, S, P, F, P, S, P]
+    L.hc_clip_grad_norm.argtypes = [PP, PP, PS, PI, S, I, F, P, P, S, P]
+    L.hc_embedding.argtypes = [P, I, S, P, I, S, S, S, I64, F, P, S, P]
+    L.hc_embedding_grad_workspace_bytes.argtypes = [S, S, S]
+    L.hc_embedding_grad.argtypes = [P, I, S, P, I, S, S, S, I64, I64, F, P, I, S, I, P, S, P]
+    L.hc_expert_rows_bound.argtypes = [S, I, I, I]
+    L.hc_expert_sort_workspace_bytes.argtypes = [S, I]
+    L.hc_expert_sort.argtypes = [P, I, I64, PE, P, S, P]
+    L.hc_expert_dispatch.argtypes = [P, I, S, S, PE, P, S, P]
+    L.hc_expert_combine.argtypes = [P, I, S, S, PE, P, P, S, P]
+    L.hc_expert_combine_grad.argtypes = [P, I, S, S, P, S, PE, P, P, S, P, P]
+    for name in ("hc_grad_norm_workspace_bytes", "hc_embedding_grad_workspace_bytes", "hc_expert_rows_bound",
+                 "hc_expert_sort_workspace_bytes"):
+        getattr(L, name).restype = S
     L.hc_step_count.argtypes = [I, I]
     L.hc_step_count.restype = I
     L.hc_ring_tasks.restype = S
@@ -114,7 +147,9 @@ def load(path: str = LIB_PATH):
                  "hc_compress_bf16_scoped", "hc_compress_bf16_entropy", "hc_compress_bf16_staged",
                  "hc_compress_bf16_noalloc", "hc_decompress_bf16",
                  "hc_decompress_bf16_entropy", "hc_compressed_allreduce", "hc_stream_create_cu_budget",
-                 "hc_stream_destroy", "hc_cu_census", "hc_stream_create_cu_range"):
+                 "hc_stream_destroy", "hc_cu_census", "hc_stream_create_cu_range", "hc_grad_norm", "hc_clip_grads",
+                 "hc_clip_grad_norm", "hc_embedding", "hc_embedding_grad", "hc_expert_sort", "hc_expert_dispatch",
+                 "hc_expert_combine", "hc_expert_combine_grad"):
         getattr(L, name).restype = I
     L.hc_status_string.argtypes = [I]
     L.hc_status_string.restype = ctypes.c_char_p
@@ -456,6 +491,241 @@ def hc_compressed_allreduce(sendbufs, recvbufs, count: int | None, ws: torch.Ten
     wb = _dptr(d_wire_bytes, 8, "d_wire_bytes") if d_wire_bytes is not None else None
     _check(L.hc_compressed_allreduce(sp, rp, count, R, wsp, ws.numel() * ws.element_size(), wb,
                                      _opts(chunk_fraction, 0, step_events), _stream_handle(stream)))
+
+
+# ----------------------------------------------------------------------------- gradients
+
+_NORMS = {"l2": HC_NORM_L2, "inf": HC_NORM_INF}
+
+
+def _tensor_list(tensors, name: str):
+    """Addresses, element counts and dtypes of many device tensors.  Each must
+    be dense (any order of its dimensions), since a norm and a scaling go over
+    its storage."""
+    n = len(tensors)
+    ptrs, counts, dtypes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)(), (ctypes.c_int32 * n)()
+    for i, t in enumerate(tensors):
+        if not t.is_cuda:
+            raise ValueError(f"{name}[{i}] is not a device tensor")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"{name}[{i}] is not dense (strides {t.stride()} for shape {tuple(t.shape)})")
+        ptrs[i] = t.data_ptr()
+        counts[i] = t.numel()
+        dtypes[i] = _dtype(t)
+    return ptrs, counts, dtypes
+
+
+def _dense(t: torch.Tensor) -> bool:
+    want = 1
+    for st, size in sorted((st, size) for st, size in zip(t.stride(), t.shape) if size != 1):
+        if st != want:
+            return False
+        want *= size
+    return True
+
+
+def _outs(grads, outs):
+    if outs is None:
+        return grads
+    if len(outs) != len(grads):
+        raise ValueError("one output per gradient")
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride():
+            raise ValueError(f"outs[{i}] must have the dtype, shape and strides of grads[{i}]")
+    return outs
+
+
+def hc_grad_norm_workspace_bytes(ntensors: int) -> int:
+    return int(load().hc_grad_norm_workspace_bytes(ntensors))
+
+
+def hc_grad_norm(grads, d_norm: torch.Tensor, ws: torch.Tensor, *, norm: str = "l2", stream=None):
+    """d_norm[0] = the norm of all grads as one vector ("l2" or "inf"); see
+    include/hc.h."""
+    L = load()
+    p, c, d = _tensor_list(grads, "grads")
+    np_ = _fptr(d_norm, 1, "d_norm")
+    _check(L.hc_grad_norm(p, c, d, len(grads), _NORMS[norm], np_, _dptr(ws, 1, "ws"), ws.numel() * ws.element_size(),
+                          _stream_handle(stream)))
+
+
+def hc_clip_grads(grads, d_norm: torch.Tensor, max_norm: float, ws: torch.Tensor, *, outs=None, stream=None):
+    """outs = grads * min(1, max_norm / (d_norm[0] + 1e-6)); in place when
+    outs is None."""
+    L = load()
+    p, c, d = _tensor_list(grads, "grads")
+    o = p if outs is None else _tensor_list(_outs(grads, outs), "outs")[0]
+    np_ = _fptr(d_norm, 1, "d_norm")
+    _check(L.hc_clip_grads(p, o, c, d, len(grads), np_, float(max_norm), _dptr(ws, 1, "ws"),
+                           ws.numel() * ws.element_size(), _stream_handle(stream)))
+
+
+def hc_clip_grad_norm(grads, max_norm: float, d_norm: torch.Tensor, ws: torch.Tensor, *, outs=None, norm: str = "l2",
+                      stream=None):
+    """hc_grad_norm and hc_clip_grads in one call; d_norm[0] receives the norm
+    before clipping."""
+    L = load()
+    p, c, d = _tensor_list(grads, "grads")
+    o = p if outs is None else _tensor_list(_outs(grads, outs), "outs")[0]
+    np_ = _fptr(d_norm, 1, "d_norm")
+    _check(L.hc_clip_grad_norm(p, o, c, d, len(grads), _NORMS[norm], float(max_norm), np_, _dptr(ws, 1, "ws"),
+                               ws.numel() * ws.element_size(), _stream_handle(stream)))
+
+
+# ----------------------------------------------------------------------------- rows
+
+def _fptr(t: torch.Tensor, need: int, name: str) -> int:
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    return _dptr(t, 4 * need, name)
+
+
+def _ids(t: torch.Tensor, name: str):
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return t.data_ptr(), t.element_size(), t.numel()
+
+
+def _matrix(t: torch.Tensor, rows: int | None, dim: int | None, name: str):
+    """Address and row stride of a 2-D device tensor whose rows are dense."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D device tensor")
+    if rows is not None and t.shape[0] < rows or dim is not None and t.shape[1] != dim:
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs ({rows}, {dim})")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.shape[1] > 1 and t.stride(1) != 1 or stride < t.shape[1]:
+        raise ValueError(f"{name} needs dense rows that do not overlap (strides {t.stride()})")
+    return t.data_ptr(), stride
+
+
+def _same_dtype(*tensors):
+    if any(t.dtype != tensors[0].dtype for t in tensors):
+        raise TypeError("all rows need one dtype")
+    return _dtype(tensors[0])
+
+
+def hc_embedding(ids: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *, vocab_start: int = 0,
+                 scale: float = 1.0, stream=None):
+    """out[t] = scale * weight[ids[t] - vocab_start], zero for an id outside
+    the table's range; see include/hc.h."""
+    L = load()
+    dt = _same_dtype(weight, out)
+    ip, ib, n = _ids(ids, "ids")
+    dim = weight.shape[-1]
+    wp, wst = _matrix(weight, None, dim, "weight")
+    op, ost = _matrix(out, n, dim, "out")
+    _check(L.hc_embedding(ip, ib, n, wp, dt, weight.shape[0], dim, wst, vocab_start, float(scale), op, ost,
+                          _stream_handle(stream)))
+
+
+def hc_embedding_grad_workspace_bytes(ntokens: int, vocab: int, dim: int) -> int:
+    return int(load().hc_embedding_grad_workspace_bytes(ntokens, vocab, dim))
+
+
+def hc_embedding_grad(ids: torch.Tensor, dout: torch.Tensor, dweight: torch.Tensor, ws: torch.Tensor, *,
+                      vocab_start: int = 0, padding_id: int | None = None, scale: float = 1.0,
+                      accumulate: bool = False, stream=None):
+    """dweight[v] = scale * the sum of dout over the tokens with id
+    vocab_start + v (added to dweight when accumulate); see include/hc.h."""
+    L = load()
+    ip, ib, n = _ids(ids, "ids")
+    dim = dweight.shape[-1]
+    dp, dst = _matrix(dout, n, dim, "dout")
+    wp, wst = _matrix(dweight, None, dim, "dweight")
+    _check(L.hc_embedding_grad(ip, ib, n, dp, _dtype(dout), dst, dweight.shape[0], dim, vocab_start,
+                               -1 if padding_id is None else padding_id, float(scale), wp, _dtype(dweight), wst,
+                               int(accumulate), _dptr(ws, 0, "ws"), ws.numel() * ws.element_size(),
+                               _stream_handle(stream)))
+
+
+# ----------------------------------------------------------------------------- experts
+
+def hc_expert_rows_bound(ntokens: int, k: int, nexperts: int, row_align: int = 1) -> int:
+    return int(load().hc_expert_rows_bound(ntokens, k, nexperts, row_align))
+
+
+def hc_expert_sort_workspace_bytes(nslots: int, nexperts: int) -> int:
+    return int(load().hc_expert_sort_workspace_bytes(nslots, nexperts))
+
+
+class ExpertPlan:
+    """The layout of tokens by expert (hc_expert_plan_t): the sizes and the
+    device tensors that hc_expert_sort writes and the other expert calls read.
+    ``for_sizes`` allocates the tensors."""
+
+    def __init__(self, ntokens: int, k: int, nexperts: int, row_align: int, row_of_slot: torch.Tensor,
+                 slot_of_row: torch.Tensor, expert_offsets: torch.Tensor, expert_counts: torch.Tensor):
+        self.ntokens, self.k, self.nexperts, self.row_align = ntokens, k, nexperts, row_align
+        self.row_of_slot, self.slot_of_row = row_of_slot, slot_of_row
+        self.expert_offsets, self.expert_counts = expert_offsets, expert_counts
+        for name, t, need in (("row_of_slot", row_of_slot, ntokens * k), ("slot_of_row", slot_of_row, 0),
+                              ("expert_offsets", expert_offsets, nexperts + 1),
+                              ("expert_counts", expert_counts, nexperts)):
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be int32")
+            _dptr(t, 4 * need, name)
+        self.rows = slot_of_row.numel()
+        self._c = hc_expert_plan_t(ntokens, k, nexperts, row_align, self.rows, row_of_slot.data_ptr(),
+                                   slot_of_row.data_ptr(), expert_offsets.data_ptr(), expert_counts.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def for_sizes(cls, ntokens: int, k: int, nexperts: int, row_align: int = 1, device="cuda"):
+        sizes = (ntokens * k, hc_expert_rows_bound(ntokens, k, nexperts, row_align), nexperts + 1, nexperts)
+        return cls(ntokens, k, nexperts, row_align,
+                   *(torch.empty(n, dtype=torch.int32, device=device) for n in sizes))
+
+
+def hc_expert_sort(experts: torch.Tensor, plan: ExpertPlan, ws: torch.Tensor | None = None, *, expert_start: int = 0,
+                   stream=None):
+    """Lays the slots of experts (ntokens x k ids) out by expert in plan; ws:
+    hc_expert_sort_workspace_bytes bytes, may be None where that is 0."""
+    L = load()
+    ip, ib, n = _ids(experts, "experts")
+    if n != plan.ntokens * plan.k:
+        raise ValueError(f"experts holds {n} ids, the plan {plan.ntokens} x {plan.k}")
+    wsp = _dptr(ws, 0, "ws") if ws is not None else None
+    _check(L.hc_expert_sort(ip, ib, expert_start, plan._ref, wsp, ws.numel() * ws.element_size() if ws is not None else 0,
+                            _stream_handle(stream)))
+
+
+def hc_expert_dispatch(x: torch.Tensor, plan: ExpertPlan, rows: torch.Tensor, *, stream=None):
+    """rows[row_of_slot[t * k + j]] = x[t]; the experts' padding rows become zero."""
+    L = load()
+    dt = _same_dtype(x, rows)
+    dim = x.shape[-1]
+    xp, xst = _matrix(x, plan.ntokens, dim, "x")
+    rp, rst = _matrix(rows, plan.rows, dim, "rows")
+    _check(L.hc_expert_dispatch(xp, dt, dim, xst, plan._ref, rp, rst, _stream_handle(stream)))
+
+
+def hc_expert_combine(rows: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor | None, out: torch.Tensor, *,
+                      stream=None):
+    """out[t] = the sum over t's slots of weight * row (weights None: plain
+    sum, the gradient of hc_expert_dispatch)."""
+    L = load()
+    dt = _same_dtype(rows, out)
+    dim = rows.shape[-1]
+    rp, rst = _matrix(rows, plan.rows, dim, "rows")
+    op, ost = _matrix(out, plan.ntokens, dim, "out")
+    wp = _fptr(weights, plan.ntokens * plan.k, "weights") if weights is not None else None
+    _check(L.hc_expert_combine(rp, dt, dim, rst, plan._ref, wp, op, ost, _stream_handle(stream)))
+
+
+def hc_expert_combine_grad(dout: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor,
+                           drows: torch.Tensor, dweights: torch.Tensor, *, stream=None):
+    """The gradients of hc_expert_combine: drows by row, dweights by slot."""
+    L = load()
+    dt = _same_dtype(dout, rows, drows)
+    dim = rows.shape[-1]
+    dp, dst = _matrix(dout, plan.ntokens, dim, "dout")
+    rp, rst = _matrix(rows, plan.rows, dim, "rows")
+    gp, gst = _matrix(drows, plan.rows, dim, "drows")
+    wp = _fptr(weights, plan.ntokens * plan.k, "weights")
+    dwp = _fptr(dweights, plan.ntokens * plan.k, "dweights")
+    _check(L.hc_expert_combine_grad(dp, dt, dim, dst, rp, rst, plan._ref, wp, gp, gst, dwp, _stream_handle(stream)))
 
 
 # ----------------------------------------------------------------------------- streams

@@ -1,0 +1,465 @@
+// embed_kernels.hip -- embedding lookup with scaling, and the table's
+// gradient from tokens sorted by id, for gfx950.
+//
+//   out[t]     = round(scale * weight[key_t])          zero where t has no key
+//   dweight[v] = round(scale * sum_{t: key_t = v} dout[t])
+//
+// The lookup streams rows.  The gradient never adds with atomics: the ids are
+// sorted (stable), the sorted list is cut into chunks of C tokens, and a wave
+// sums one chunk's rows over 64 vectors of columns, writing each run of equal
+// keys that lies inside the chunk straight to its row.  A run that crosses a
+// chunk's edge leaves fp32 partials, which a second launch adds in order; so
+// a token that fills half the batch is spread over as many waves as its
+// chunks.  Rows without a token are zeroed by further waves of the first
+// launch, each of which looks 16 rows up in the sorted list.
+#include "key_sort.hpp"
+#include "launch.hpp"
+
+namespace hc {
+namespace {
+
+constexpr uint32_t kMaxBlocks = 1u << 22;
+
+inline uint32_t blocks_for(uint64_t waves) {
+  const uint64_t b = (waves + kWaves - 1) / kWaves;
+  return (uint32_t)(b < kMaxBlocks ? b : kMaxBlocks);
+}
+
+// ---------------------------------------------------------------- lookup
+
+// A wave handles 64 >> lg rows of 1 << lg vectors (lg < 6: narrow tables), or
+// a slice of U * 64 vectors of one row (lg == 6).
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size_t ntokens, const void* weight,
+                                                             uint32_t dim, size_t wstride, float scale, void* out,
+                                                             size_t ostride, uint32_t lg, uint32_t slices,
+                                                             uint64_t units) {
+  const uint32_t nvec = (dim + T::kVec - 1) / T::kVec;
+  const uint32_t sub = lane_id() >> lg, at = lane_id() & ((1u << lg) - 1);
+  for (uint64_t u = (uint64_t)blockIdx.x * kWaves + wave_id(); u < units; u += (uint64_t)gridDim.x * kWaves) {
+    const size_t t = u / slices * (64u >> lg) + sub;
+    const uint32_t v0 = (uint32_t)(u % slices) * (64 * U) + at;
+    if (t >= ntokens) continue;
+    const uint32_t key = load_key(src, t);
+    vec4 x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t v = v0 + 64 * i;
+      x[i] = vec4{0, 0, 0, 0};
+      if (key != kNoKey && v < nvec)
+        x[i] = load_vec<T>(elem<T>(weight, (size_t)key * wstride + (size_t)v * T::kVec), dim - v * T::kVec);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t v = v0 + 64 * i;
+      if (v >= nvec) continue;
+      float f[T::kVec];
+      T::unpack(x[i], f);
+#pragma unroll
+      for (int j = 0; j < T::kVec; ++j) f[j] *= scale;
+      store_vec<T>(elem<T>(out, t * ostride + (size_t)v * T::kVec), key == kNoKey ? vec4{0, 0, 0, 0} : T::pack(f),
+                   dim - v * T::kVec);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sorting the ids
+
+constexpr uint32_t kRankMax = 4096;     // ids sorted by counting smaller ones, in one launch
+
+// Each workgroup places 64 ids: its 16 waves compare them with a sixteenth of
+// all ids each.  n^2 comparisons, 2 instructions each, beat the launches of a
+// radix sort while n is small.
+__global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint32_t n, uint32_t* keys, uint32_t* pos) {
+  __shared__ __attribute__((aligned(16))) uint32_t all[kRankMax];
+  __shared__ uint32_t part[kSortWaves][64];
+  const uint32_t padded = (n + 63) & ~63u;
+  for (uint32_t i = threadIdx.x; i < padded; i += kSortThreads) {
+    const uint32_t k = i < n ? load_key(src, i) : kNoKey;
+    all[i] = k < src.nkeys ? k : src.nkeys;     // no key sorts last
+  }
+  __syncthreads();
+  const uint32_t g0 = blockIdx.x * 64, i = g0 + lane_id();
+  const uint32_t key = all[i];
+  const uint32_t share = padded / kSortWaves;    // a multiple of 4
+  const uint32_t lo = wave_id() * share, hi = lo + share;
+  uint32_t c = 0;
+  auto count4 = [&](uint32_t j, uint32_t below) {
+    const vec4 k = *reinterpret_cast<const vec4*>(&all[j]);
+    c += (k[0] < below) + (k[1] < below) + (k[2] < below) + (k[3] < below);
+  };
+  uint32_t j = lo;
+  for (; j < hi && j < g0; j += 4) count4(j, key + 1);          // earlier ids: equal ones come first
+  for (; j < hi && j < g0 + 64; ++j) c += all[j] < key + (j < i ? 1 : 0);
+  for (; j < hi; j += 4) count4(j, key);                        // later ids
+  part[threadIdx.x >> 6][lane_id()] = c;
+  __syncthreads();
+  if (threadIdx.x < 64 && i < n) {
+    uint32_t r = 0;
+    for (uint32_t w = 0; w < kSortWaves; ++w) r += part[w][threadIdx.x];
+    if (r < n) {
+      keys[r] = key < src.nkeys ? key : kNoKey;
+      pos[r] = i;
+    }
+  }
+}
+
+// One digit of a least-significant-digit radix sort.  The first pass reads
+// the ids, later ones the pairs that the pass before wrote.
+struct Pass {
+  KeySource src;
+  const uint32_t* keys;     // NULL: the ids of src
+  const uint32_t* pos;
+  uint32_t n, tile, tiles, shift, bits;
+  uint32_t* hist;
+  uint32_t* keys_out;
+  uint32_t* pos_out;
+};
+
+__device__ __forceinline__ uint32_t pass_digit(const Pass& p, size_t i) {
+  const uint32_t k = p.keys ? p.keys[i] : load_key(p.src, i);
+  return k == kNoKey ? kNoKey : (k >> p.shift) & ((1u << p.bits) - 1);
+}
+
+__global__ void __launch_bounds__(kSortThreads) pass_histogram_kernel(Pass p) {
+  __shared__ uint32_t lds[kMaxRadix];
+  const uint32_t radix = 1u << p.bits;
+  const size_t lo = (size_t)blockIdx.x * p.tile;
+  const size_t hi = lo + p.tile < p.n ? lo + p.tile : p.n;
+  tile_histogram(lds, radix, lo, hi, [&](size_t i) { return pass_digit(p, i); }, p.hist + (size_t)blockIdx.x * radix);
+}
+
+__global__ void __launch_bounds__(kSortThreads) pass_scatter_kernel(Pass p) {
+  __shared__ uint32_t counts[kSortWaves * kMaxRadix];
+  __shared__ uint32_t scan[kSortWaves];
+  const uint32_t radix = 1u << p.bits;
+  const size_t lo = (size_t)blockIdx.x * p.tile;
+  const size_t hi = lo + p.tile < p.n ? lo + p.tile : p.n;
+  uint32_t before, total, all;
+  tile_sums(p.hist, radix, p.tiles, blockIdx.x, threadIdx.x, &before, &total);
+  const uint32_t first = block_scan(total, scan, &all);
+  place_items(counts, radix, p.bits, lo, hi, p.tile, first + before, [&](size_t i) { return pass_digit(p, i); },
+              [&](size_t i, uint32_t d, uint32_t place) {
+                if (d != kNoKey && place < p.n) {
+                  p.keys_out[place] = p.keys ? p.keys[i] : load_key(p.src, i);
+                  p.pos_out[place] = p.pos ? p.pos[i] : (uint32_t)i;
+                }
+                if (i >= all) {       // behind the last id with a key
+                  p.keys_out[i] = kNoKey;
+                  p.pos_out[i] = 0;
+                }
+              });
+}
+
+}  // namespace
+
+constexpr size_t kHistBytes = (size_t)kMaxTiles * kMaxRadix * sizeof(uint32_t);
+
+size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
+  (void)nkeys;
+  return n <= kRankMax ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
+}
+
+hipError_t launch_sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws,
+                           hipStream_t stream) {
+  if (n == 0) return hipSuccess;
+  if (n <= kRankMax) {
+    rank_kernel<<<(uint32_t)((n + 63) / 64), kSortThreads, 0, stream>>>(src, (uint32_t)n, keys, pos);
+    return hipGetLastError();
+  }
+  uint32_t bits = 1;
+  while (bits < 32 && ((uint64_t)src.nkeys - 1) >> bits) ++bits;
+  const uint32_t passes = (bits + 9) / 10, per = (bits + passes - 1) / passes;
+  uint32_t* hist = static_cast<uint32_t*>(ws);
+  uint32_t* tmp_keys = hist + (size_t)kMaxTiles * kMaxRadix;
+  uint32_t* tmp_pos = tmp_keys + n;
+  Pass p = {src, nullptr, nullptr, (uint32_t)n, sort_tile(n), sort_tiles(n), 0, per, hist, nullptr, nullptr};
+  for (uint32_t k = 0; k < passes; ++k) {
+    const bool last_buffer = ((passes - 1 - k) & 1) == 0;   // the last pass ends in keys/pos
+    p.shift = k * per;
+    p.bits = per;
+    p.keys_out = last_buffer ? keys : tmp_keys;
+    p.pos_out = last_buffer ? pos : tmp_pos;
+    pass_histogram_kernel<<<p.tiles, kSortThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    pass_scatter_kernel<<<p.tiles, kSortThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    p.keys = p.keys_out;
+    p.pos = p.pos_out;
+  }
+  return hipSuccess;
+}
+
+// ---------------------------------------------------------------- the gradient
+
+namespace {
+
+constexpr uint32_t kZeroRows = 16;      // table rows per zeroing wave
+constexpr uint32_t kJoinCols = 256;     // columns per workgroup and round of the join: 4 fp32 per lane
+
+struct Grad {
+  const uint32_t* keys;     // sorted
+  const uint32_t* pos;
+  uint32_t n, chunk, nchunks, dim, slices;
+  uint32_t vocab;
+  const void* dout;
+  size_t dstride;
+  float scale;
+  void* dweight;
+  size_t wstride;
+  float* partial;           // [chunk][2][pstride]: a run that began before the chunk; one that goes on after it
+  uint32_t pstride;
+  uint64_t sum_units, units;
+};
+
+template <typename To, int N, bool ACC>
+__device__ __forceinline__ void write_row(const Grad& g, uint32_t row, uint32_t col, const float* sum) {
+  typename To::raw* p = elem<To>(g.dweight, (size_t)row * g.wstride + col);
+  const uint32_t left = g.dim - col;
+  float f[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = sum[i] * g.scale;
+  if constexpr (ACC) {
+    float old[N];
+    load_vals<To, N>(p, old, left);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] += old[i];
+  }
+  store_vals<To, N>(p, f, left);
+}
+
+template <typename Ti, typename To, bool ACC>
+__device__ __forceinline__ void sum_chunk(const Grad& g, uint32_t c, uint32_t slice) {
+  constexpr int N = Ti::kVec, U = 8;
+  const uint32_t lane = lane_id();
+  const uint32_t p0 = c * g.chunk;
+  const uint32_t cnt = g.n - p0 < g.chunk ? g.n - p0 : g.chunk;
+  const uint32_t key = lane < cnt ? g.keys[p0 + lane] : kNoKey;
+  const uint32_t pos = lane < cnt ? g.pos[p0 + lane] : 0;
+  const uint32_t prev = p0 ? g.keys[p0 - 1] : kNoKey;
+  const uint32_t next = p0 + cnt < g.n ? g.keys[p0 + cnt] : kNoKey;
+  const uint32_t live = (uint32_t)__popcll(__ballot(key != kNoKey));    // the keys come first
+  if (!live) return;
+  uint32_t after = __shfl_down(key, 1);
+  if (lane == cnt - 1) after = next;
+  const uint64_t ends = __ballot(lane < live && (key != after || lane == live - 1));
+  const bool head = first_lane_read(key) == first_lane_read(prev);
+  const bool tail = lane_read(key, live - 1) == lane_read(after, live - 1);
+  const uint32_t col = slice * 64 * N + lane * N;
+  const bool mine = col < g.dim;
+  const uint32_t left = mine ? g.dim - col : 0;
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+  bool first_run = true;
+  for (uint32_t i = 0; i < live; i += U) {
+    vec4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u] = vec4{0, 0, 0, 0};
+      if (i + u < live) {
+        const uint32_t row = lane_read(pos, i + u);
+        if (mine) x[u] = load_vec<Ti>(elem<Ti>(g.dout, (size_t)row * g.dstride + col), left);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= live) break;
+      float f[N];
+      Ti::unpack(x[u], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] += f[j];
+      if (!((ends >> (i + u)) & 1)) continue;
+      const bool from_before = first_run && head;
+      const bool goes_on = i + u == live - 1 && tail;
+      first_run = false;
+      const uint32_t table_row = lane_read(key, i + u);
+      if (mine) {
+        if (from_before || goes_on)
+          store_vals<F32, N>(elem<F32>(g.partial, ((size_t)c * 2 + (from_before ? 0 : 1)) * g.pstride + col), acc,
+                             left);
+        else
+          write_row<To, N, ACC>(g, table_row, col, acc);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    }
+  }
+}
+
+template <typename To>
+__device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
+  const uint32_t lane = lane_id(), v = v0 + lane;
+  const bool ask = lane < kZeroRows && v < g.vocab;
+  uint32_t lo = 0, hi = ask ? g.n : 0;       // the first place whose key is not below v
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (g.keys[mid] < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  uint64_t absent = __ballot(ask && (lo == g.n || g.keys[lo] != v));
+  while (absent) {
+    const uint32_t k = (uint32_t)__builtin_ctzll(absent);
+    absent &= absent - 1;
+    typename To::raw* row = elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride);
+    for (uint32_t col = lane * To::kVec; col < g.dim; col += 64 * To::kVec)
+      store_vec<To>(row + col, vec4{0, 0, 0, 0}, g.dim - col);
+  }
+}
+
+template <typename Ti, typename To, bool ACC>
+__global__ void __launch_bounds__(kThreads) grad_kernel(Grad g) {
+  for (uint64_t u = (uint64_t)blockIdx.x * kWaves + wave_id(); u < g.units; u += (uint64_t)gridDim.x * kWaves) {
+    if (u < g.sum_units)
+      sum_chunk<Ti, To, ACC>(g, (uint32_t)(u / g.slices), (uint32_t)(u % g.slices));
+    else if constexpr (!ACC)
+      zero_rows<To>(g, (uint32_t)(u - g.sum_units) * kZeroRows);
+  }
+}
+
+// Adds the partials of the runs that cross chunk edges.  The chunk in which
+// such a run begins owns it; its 4 waves take every fourth of the chunks that
+// follow, and wave 0 adds the four sums in order.
+template <typename To, bool ACC>
+__global__ void __launch_bounds__(kThreads) join_kernel(Grad g) {
+  __shared__ float lds[kWaves][kJoinCols];
+  const uint32_t lane = lane_id(), w = wave_id();
+  for (uint32_t c = blockIdx.x; c + 1 < g.nchunks; c += gridDim.x) {
+    const uint32_t p0 = c * g.chunk, p1 = p0 + g.chunk;
+    const uint32_t key = g.keys[p1 - 1];
+    if (key == kNoKey || g.keys[p1] != key) continue;
+    if (p0 && g.keys[p0] == key && g.keys[p0 - 1] == key) continue;   // it began before this chunk
+    uint32_t more = 0;     // chunks after c that begin inside the run
+    for (;;) {
+      const uint32_t k = c + 1 + more + lane;
+      const uint64_t same = __ballot(k < g.nchunks && g.keys[(size_t)k * g.chunk] == key);
+      const uint32_t run = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
+      more += run;
+      if (run < 64) break;
+    }
+    for (uint32_t col = blockIdx.y * kJoinCols + lane * 4; col - lane * 4 < g.dim; col += gridDim.y * kJoinCols) {
+      float acc[4] = {0, 0, 0, 0};
+      if (col < g.dim) {
+#pragma unroll 4
+        for (uint32_t i = w; i < more; i += kWaves) {
+          const float* p = g.partial + (size_t)(c + 1 + i) * 2 * g.pstride + col;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] += p[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lds[w][lane * 4 + j] = acc[j];
+      __syncthreads();
+      if (w == 0 && col < g.dim) {
+        const float* p = g.partial + ((size_t)c * 2 + 1) * g.pstride + col;
+        float sum[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[j] = p[j];
+          for (int k = 0; k < kWaves; ++k) sum[j] += lds[k][lane * 4 + j];
+        }
+        write_row<To, 4, ACC>(g, key, col, sum);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Tokens per chunk (<= 64): as many as leave some 4096 waves to the sums.
+uint32_t chunk_tokens(size_t n, size_t dim) {
+  const size_t slices = (dim + 255) / 256;
+  if (n * slices >= (size_t)4096 * 32) return 32;
+  if (n * slices >= (size_t)4096 * 16) return 16;
+  return 8;
+}
+
+struct GradLayout {
+  size_t keys, pos, sort, partial, bytes;
+};
+GradLayout grad_layout(size_t n, size_t vocab, size_t dim) {
+  auto up = [](size_t x) { return (x + 15) & ~(size_t)15; };
+  const uint32_t chunk = chunk_tokens(n, dim);
+  GradLayout l;
+  l.keys = 0;
+  l.pos = up(n * 4);
+  l.sort = l.pos + up(n * 4);
+  l.partial = l.sort + up(sort_ids_ws_bytes(n, vocab));
+  l.bytes = l.partial + (n + chunk - 1) / chunk * 2 * ((dim + 3) / 4 * 4) * sizeof(float);
+  return l;
+}
+
+template <typename Ti, typename To, bool ACC>
+hipError_t run_grad(const Grad& g, hipStream_t stream) {
+  if (g.units) {
+    grad_kernel<Ti, To, ACC><<<blocks_for(g.units), kThreads, 0, stream>>>(g);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  if (g.nchunks > 1) {
+    const uint32_t cols = (g.dim + kJoinCols - 1) / kJoinCols;
+    join_kernel<To, ACC><<<dim3(g.nchunks - 1 < 65536 ? g.nchunks - 1 : 65536, cols < 8 ? cols : 8), kThreads, 0, stream>>>(g);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* weight, hc_dtype_t dtype, size_t dim,
+                            size_t wstride, float scale, void* out, size_t ostride, hipStream_t stream) {
+  constexpr int U = 2;
+  const uint32_t nvec = (uint32_t)((dim + (dtype == HC_F32 ? 3 : 7)) / (dtype == HC_F32 ? 4 : 8));
+  uint32_t lg = 0;
+  while (lg < 6 && (1u << lg) < nvec) ++lg;
+  const uint32_t slices = (nvec + 64 * U - 1) / (64 * U);
+  const uint64_t units = (uint64_t)((ntokens + (64u >> lg) - 1) / (64u >> lg)) * slices;
+  if (dtype == HC_F32)
+    embedding_kernel<F32, U><<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride,
+                                                                         scale, out, ostride, lg, slices, units);
+  else
+    embedding_kernel<BF16, U><<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride,
+                                                                          scale, out, ostride, lg, slices, units);
+  return hipGetLastError();
+}
+
+size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) { return grad_layout(ntokens, vocab, dim).bytes; }
+
+hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const void* dout, hc_dtype_t dtype, size_t dim,
+                                 size_t dstride, float scale, void* dweight, hc_dtype_t dwtype, size_t wstride,
+                                 bool accumulate, void* ws, hipStream_t stream) {
+  const GradLayout l = grad_layout(ntokens, src.nkeys, dim);
+  char* base = static_cast<char*>(ws);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(base + l.keys);
+  uint32_t* pos = reinterpret_cast<uint32_t*>(base + l.pos);
+  if (hipError_t e = launch_sort_ids(src, ntokens, keys, pos, base + l.sort, stream); e != hipSuccess) return e;
+  Grad g = {};
+  g.keys = keys;
+  g.pos = pos;
+  g.n = (uint32_t)ntokens;
+  g.chunk = chunk_tokens(ntokens, dim);
+  g.nchunks = (g.n + g.chunk - 1) / g.chunk;
+  g.dim = (uint32_t)dim;
+  const uint32_t width = 64 * (dtype == HC_F32 ? 4 : 8);
+  g.slices = (g.dim + width - 1) / width;
+  g.vocab = src.nkeys;
+  g.dout = dout;
+  g.dstride = dstride;
+  g.scale = scale;
+  g.dweight = dweight;
+  g.wstride = wstride;
+  g.partial = reinterpret_cast<float*>(base + l.partial);
+  g.pstride = (g.dim + 3) / 4 * 4;
+  g.sum_units = (uint64_t)g.nchunks * g.slices;
+  g.units = g.sum_units + (accumulate ? 0 : (g.vocab + kZeroRows - 1) / kZeroRows);
+  if (dtype == HC_F32) {
+    if (dwtype == HC_F32)
+      return accumulate ? run_grad<F32, F32, true>(g, stream) : run_grad<F32, F32, false>(g, stream);
+    return accumulate ? run_grad<F32, BF16, true>(g, stream) : run_grad<F32, BF16, false>(g, stream);
+  }
+  if (dwtype == HC_F32)
+    return accumulate ? run_grad<BF16, F32, true>(g, stream) : run_grad<BF16, F32, false>(g, stream);
+  return accumulate ? run_grad<BF16, BF16, true>(g, stream) : run_grad<BF16, BF16, false>(g, stream);
+}
+
+}  // namespace hc

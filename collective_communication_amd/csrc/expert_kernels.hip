@@ -1,0 +1,417 @@
+// expert_kernels.hip -- tokens sorted by expert and back with weights, and
+// the gradient of the way back, for gfx950.
+//
+//   sort:      slots t * k + j laid out by expert, stable, aligned per expert
+//   dispatch:  rows[row(t, j)] = x[t]
+//   combine:   out[t] = round(sum_j w[t, j] * rows[row(t, j)])
+//   gradient:  drows[row(t, j)] = round(w[t, j] * dout[t]),  dw[t, j] = <dout[t], rows[row(t, j)]>
+//
+// All but the sort are streams over rows, organised by token: a wave reads a
+// token's slice once and writes its k copies, or reads its k rows and writes
+// one sum, so the side that is k times larger moves exactly once and the
+// other is not read k times over.  Sums run over j in order within a lane:
+// no atomics.  The token's row numbers are loaded once into the wave's lanes
+// and read from there as scalars, so every row's address is scalar.
+#include "key_sort.hpp"
+#include "launch.hpp"
+
+namespace hc {
+namespace {
+
+constexpr uint32_t kMaxBlocks = 1u << 22;
+
+inline uint32_t blocks_for(uint64_t waves) {
+  const uint64_t b = (waves + kWaves - 1) / kWaves;
+  return (uint32_t)(b < kMaxBlocks ? b : kMaxBlocks);
+}
+
+// ---------------------------------------------------------------- sort
+
+struct Sort {
+  KeySource src;
+  uint32_t n, tile, tiles, experts, bits, align, rows;
+  uint32_t* hist;
+  int32_t* row_of_slot;
+  int32_t* slot_of_row;
+  int32_t* offsets;
+  int32_t* counts;
+};
+
+__global__ void __launch_bounds__(kSortThreads) expert_histogram_kernel(Sort s) {
+  __shared__ uint32_t lds[kMaxRadix];
+  const size_t lo = (size_t)blockIdx.x * s.tile;
+  const size_t hi = lo + s.tile < s.n ? lo + s.tile : s.n;
+  tile_histogram(lds, s.experts, lo, hi, [&](size_t i) { return load_key(s.src, i); },
+                 s.hist + (size_t)blockIdx.x * s.experts);
+}
+
+// ONE: a single tile, which counts for itself (no histogram launch).
+template <bool ONE>
+__global__ void __launch_bounds__(kSortThreads) expert_scatter_kernel(Sort s) {
+  __shared__ uint32_t counts[kSortWaves * kMaxRadix];
+  __shared__ uint32_t scan[kSortWaves];
+  const size_t lo = (size_t)blockIdx.x * s.tile;
+  const size_t hi = lo + s.tile < s.n ? lo + s.tile : s.n;
+  const uint32_t e = threadIdx.x;
+  auto digit = [&](size_t i) { return load_key(s.src, i); };
+  uint32_t before = 0, total = 0, used;
+  if constexpr (ONE) {
+    for (uint32_t d = threadIdx.x; d < s.experts; d += kSortThreads) counts[d] = 0;
+    __syncthreads();
+    for (size_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+      const uint32_t d = digit(i);
+      if (d != kNoKey) atomicAdd(&counts[d], 1u);
+    }
+    __syncthreads();
+    total = e < s.experts ? counts[e] : 0;
+    __syncthreads();
+  } else {
+    tile_sums(s.hist, s.experts, s.tiles, blockIdx.x, e, &before, &total);
+  }
+  const uint32_t padded = (total + s.align - 1) / s.align * s.align;
+  const uint32_t first = block_scan(padded, scan, &used);
+  if (blockIdx.x == 0) {
+    if (e < s.experts) {
+      s.offsets[e] = (int32_t)first;
+      s.counts[e] = (int32_t)total;
+    }
+    if (e == 0) s.offsets[s.experts] = (int32_t)used;
+  }
+  // rows without a slot: each expert's padding, spread over the tiles, and
+  // what lies behind the last expert
+  if (e < s.experts && e % gridDim.x == blockIdx.x)
+    for (uint32_t r = first + total; r < first + padded; ++r) s.slot_of_row[r] = -1;
+  for (size_t r = (size_t)used + blockIdx.x * kSortThreads + e; r < s.rows; r += (size_t)gridDim.x * kSortThreads)
+    s.slot_of_row[r] = -1;
+  place_items(counts, s.experts, s.bits, lo, hi, s.tile, first + before, digit,
+              [&](size_t i, uint32_t d, uint32_t place) {
+                const bool there = d != kNoKey && place < s.rows;
+                s.row_of_slot[i] = there ? (int32_t)place : -1;
+                if (there) s.slot_of_row[place] = (int32_t)i;
+              });
+}
+
+// ---------------------------------------------------------------- rows
+
+struct Rows {
+  const int32_t* row_of_slot;
+  const int32_t* offsets;
+  const int32_t* counts;
+  const float* weights;
+  size_t ntokens;
+  uint32_t k, experts, dim, slices, align;
+  const void* x;            // by token (dispatch), or dout
+  size_t xstride;
+  const void* rows;         // by row (combine, gradient)
+  size_t rstride;
+  void* out;                // by token (combine) or by row (dispatch, gradient)
+  size_t ostride;
+  float* dweights;
+  uint64_t token_units, units;
+};
+
+// Zeroes the padding of expert e: rows [offset + count, next offset).
+template <typename T>
+__device__ __forceinline__ void zero_padding(const Rows& r, uint32_t e) {
+  const uint32_t a = (uint32_t)(r.offsets[e] + r.counts[e]), b = (uint32_t)r.offsets[e + 1];
+  for (uint32_t row = a; row < b; ++row) {
+    typename T::raw* p = elem<T>(r.out, (size_t)row * r.ostride);
+    for (uint32_t c = lane_id() * T::kVec; c < r.dim; c += 64 * T::kVec)
+      store_vec<T>(p + c, vec4{0, 0, 0, 0}, r.dim - c);
+  }
+}
+
+// A wave copies a slice of U * 64 vectors of one token to its k rows.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
+  const uint32_t lane = lane_id();
+  for (uint64_t u = (uint64_t)blockIdx.x * kWaves + wave_id(); u < r.units; u += (uint64_t)gridDim.x * kWaves) {
+    if (u >= r.token_units) {
+      zero_padding<T>(r, (uint32_t)(u - r.token_units));
+      continue;
+    }
+    const size_t t = u / r.slices;
+    const uint32_t c0 = (uint32_t)(u % r.slices) * (U * 64 * T::kVec) + lane * T::kVec;
+    const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
+    uint64_t there = __ballot(row >= 0);
+    if (!there) continue;
+    vec4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t c = c0 + i * 64 * T::kVec;
+      if (c < r.dim) v[i] = load_vec<T>(elem<T>(r.x, t * r.xstride + c), r.dim - c);
+    }
+    while (there) {
+      const uint32_t j = (uint32_t)__builtin_ctzll(there);
+      there &= there - 1;
+      const size_t base = (size_t)lane_read((uint32_t)row, j) * r.ostride;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = c0 + i * 64 * T::kVec;
+        if (c < r.dim) store_vec<T>(elem<T>(r.out, base + c), v[i], r.dim - c);
+      }
+    }
+  }
+}
+
+// A wave sums a slice of 64 vectors of one token's rows, four rows in flight.
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
+  constexpr int N = T::kVec, J = 4;
+  const uint32_t lane = lane_id();
+  for (uint64_t u = (uint64_t)blockIdx.x * kWaves + wave_id(); u < r.units; u += (uint64_t)gridDim.x * kWaves) {
+    const size_t t = u / r.slices;
+    const uint32_t c = (uint32_t)(u % r.slices) * (64 * N) + lane * N;
+    const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
+    const uint32_t w = WEIGHTED && lane < r.k ? f32_bits(r.weights[t * r.k + lane]) : f32_bits(1.0f);
+    uint64_t there = __ballot(row >= 0);
+    const bool mine = c < r.dim;    // every lane stays, for the lane reads below
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    while (there) {
+      vec4 v[J];
+      float g[J];
+#pragma unroll
+      for (int q = 0; q < J; ++q) {
+        g[q] = 0.0f;
+        v[q] = vec4{0, 0, 0, 0};
+        if (!there) continue;
+        const uint32_t j = (uint32_t)__builtin_ctzll(there);
+        there &= there - 1;
+        g[q] = bits_f32(lane_read(w, j));
+        const size_t base = (size_t)lane_read((uint32_t)row, j) * r.rstride;
+        if (mine) v[q] = load_vec<T>(elem<T>(r.rows, base + c), r.dim - c);
+      }
+#pragma unroll
+      for (int q = 0; q < J; ++q) {
+        float f[N];
+        T::unpack(v[q], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(g[q], f[i], acc[i]);
+      }
+    }
+    if (mine) store_vec<T>(elem<T>(r.out, t * r.ostride + c), T::pack(acc), r.dim - c);
+  }
+}
+
+// WPT waves share a token's slices; each row's dot product is summed over a
+// lane's slices, then over lanes and waves in a fixed order.  J slots at a
+// time: their rows' loads are in flight together with the token's.
+template <typename T, int WPT>
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(Rows r) {
+  constexpr int N = T::kVec, J = 4;
+  __shared__ float part[kWaves][J];
+  const uint32_t lane = lane_id(), wave = wave_id();
+  const uint32_t sub = wave % WPT;
+  const uint64_t step = (uint64_t)gridDim.x * (kWaves / WPT);
+  for (uint64_t u = (uint64_t)blockIdx.x * (kWaves / WPT) + wave / WPT; u < r.units; u += step) {
+    if (u >= r.token_units) {
+      // with WPT > 1 the workgroup's waves take this unit's experts in turn
+      const uint32_t e = (uint32_t)(u - r.token_units) * WPT + sub;
+      if (e < r.experts) zero_padding<T>(r, e);
+      continue;
+    }
+    const size_t t = u;
+    const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
+    const uint32_t w = lane < r.k ? f32_bits(r.weights[t * r.k + lane]) : 0;
+    uint64_t there = __ballot(row >= 0);
+    float dw = 0.0f;        // lane j: slot j's
+    while (there) {
+      float dot[J], g[J];
+      uint32_t slot[J];
+      size_t rbase[J], obase[J];
+      int live = 0;
+#pragma unroll
+      for (int q = 0; q < J; ++q) {
+        dot[q] = 0.0f;
+        slot[q] = 64;
+        g[q] = 0.0f;
+        rbase[q] = obase[q] = 0;
+        if (!there) continue;
+        slot[q] = (uint32_t)__builtin_ctzll(there);
+        there &= there - 1;
+        const size_t at = lane_read((uint32_t)row, slot[q]);
+        rbase[q] = at * r.rstride;
+        obase[q] = at * r.ostride;
+        g[q] = bits_f32(lane_read(w, slot[q]));
+        live = q + 1;
+      }
+      for (uint32_t c = (sub * 64 + lane) * N; c < r.dim; c += WPT * 64 * N) {
+        vec4 v[J];
+        const vec4 d = load_vec<T>(elem<T>(r.x, t * r.xstride + c), r.dim - c);
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+          v[q] = vec4{0, 0, 0, 0};
+          if (q < live) v[q] = load_vec<T>(elem<T>(r.rows, rbase[q] + c), r.dim - c);
+        }
+        float fd[N];
+        T::unpack(d, fd);
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+          if (q >= live) continue;
+          float f[N], o[N];
+          T::unpack(v[q], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[q] = __builtin_fmaf(fd[i], f[i], dot[q]);
+            o[i] = g[q] * fd[i];
+          }
+          store_vec<T>(elem<T>(r.out, obase[q] + c), T::pack(o), r.dim - c);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < J; ++q) {
+#pragma unroll
+        for (int m = 32; m; m >>= 1) dot[q] += __shfl_xor(dot[q], m);
+      }
+      if constexpr (WPT > 1) {
+        if (lane == 0) {
+#pragma unroll
+          for (int q = 0; q < J; ++q) part[wave][q] = dot[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+          dot[q] = 0.0f;
+          for (int v = 0; v < WPT; ++v) dot[q] += part[v][q];
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int q = 0; q < J; ++q)
+        if (lane == slot[q]) dw = dot[q];
+    }
+    if (sub == 0 && lane < r.k) r.dweights[t * r.k + lane] = dw;
+  }
+}
+
+constexpr int kDispatchU = 2;
+
+Rows rows_of(const hc_expert_plan_t& plan, size_t dim) {
+  Rows r = {};
+  r.row_of_slot = plan.row_of_slot;
+  r.offsets = plan.expert_offsets;
+  r.counts = plan.expert_counts;
+  r.ntokens = plan.ntokens;
+  r.k = (uint32_t)plan.k;
+  r.experts = (uint32_t)plan.nexperts;
+  r.align = (uint32_t)plan.row_align;
+  r.dim = (uint32_t)dim;
+  return r;
+}
+
+}  // namespace
+
+size_t expert_sort_ws_bytes(size_t nslots, size_t nexperts) {
+  const size_t tiles = sort_tiles(nslots);
+  return tiles <= 1 ? 0 : tiles * nexperts * sizeof(uint32_t);
+}
+
+hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan, void* ws, hipStream_t stream) {
+  Sort s = {};
+  s.src = src;
+  s.n = (uint32_t)(plan.ntokens * (size_t)plan.k);
+  s.tile = sort_tile(s.n);
+  s.tiles = sort_tiles(s.n);
+  s.experts = (uint32_t)plan.nexperts;
+  s.bits = 0;
+  while ((s.experts - 1) >> s.bits) ++s.bits;
+  s.align = (uint32_t)plan.row_align;
+  s.rows = (uint32_t)plan.rows;
+  s.hist = static_cast<uint32_t*>(ws);
+  s.row_of_slot = plan.row_of_slot;
+  s.slot_of_row = plan.slot_of_row;
+  s.offsets = plan.expert_offsets;
+  s.counts = plan.expert_counts;
+  if (s.tiles <= 1) {
+    expert_scatter_kernel<true><<<1, kSortThreads, 0, stream>>>(s);
+    return hipGetLastError();
+  }
+  expert_histogram_kernel<<<s.tiles, kSortThreads, 0, stream>>>(s);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  expert_scatter_kernel<false><<<s.tiles, kSortThreads, 0, stream>>>(s);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_dispatch(const void* x, hc_dtype_t dtype, size_t dim, size_t xstride,
+                                  const hc_expert_plan_t& plan, void* rows, size_t rstride, hipStream_t stream) {
+  Rows r = rows_of(plan, dim);
+  const uint32_t width = kDispatchU * 64 * (dtype == HC_F32 ? 4 : 8);
+  r.slices = (r.dim + width - 1) / width;
+  r.x = x;
+  r.xstride = xstride;
+  r.out = rows;
+  r.ostride = rstride;
+  r.token_units = (uint64_t)r.ntokens * r.slices;
+  r.units = r.token_units + (r.align > 1 ? r.experts : 0);
+  if (!r.units) return hipSuccess;
+  if (dtype == HC_F32)
+    dispatch_kernel<F32, kDispatchU><<<blocks_for(r.units), kThreads, 0, stream>>>(r);
+  else
+    dispatch_kernel<BF16, kDispatchU><<<blocks_for(r.units), kThreads, 0, stream>>>(r);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(const void* rows, hc_dtype_t dtype, size_t dim, size_t rstride,
+                                 const hc_expert_plan_t& plan, const float* weights, void* out, size_t ostride,
+                                 hipStream_t stream) {
+  Rows r = rows_of(plan, dim);
+  const uint32_t width = 64 * (dtype == HC_F32 ? 4 : 8);
+  r.slices = (r.dim + width - 1) / width;
+  r.rows = rows;
+  r.rstride = rstride;
+  r.weights = weights;
+  r.out = out;
+  r.ostride = ostride;
+  r.units = (uint64_t)r.ntokens * r.slices;
+  if (!r.units) return hipSuccess;
+  const uint32_t blocks = blocks_for(r.units);
+  if (dtype == HC_F32) {
+    if (weights)
+      combine_kernel<F32, true><<<blocks, kThreads, 0, stream>>>(r);
+    else
+      combine_kernel<F32, false><<<blocks, kThreads, 0, stream>>>(r);
+  } else {
+    if (weights)
+      combine_kernel<BF16, true><<<blocks, kThreads, 0, stream>>>(r);
+    else
+      combine_kernel<BF16, false><<<blocks, kThreads, 0, stream>>>(r);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_grad(const void* dout, hc_dtype_t dtype, size_t dim, size_t dstride,
+                                      const void* rows, size_t rstride, const hc_expert_plan_t& plan,
+                                      const float* weights, void* drows, size_t drstride, float* dweights,
+                                      hipStream_t stream) {
+  Rows r = rows_of(plan, dim);
+  r.x = dout;
+  r.xstride = dstride;
+  r.rows = rows;
+  r.rstride = rstride;
+  r.weights = weights;
+  r.out = drows;
+  r.ostride = drstride;
+  r.dweights = dweights;
+  r.token_units = r.ntokens;
+  // one wave per token fills the GPU from some 4096 tokens on
+  const int wpt = r.ntokens >= 4096 ? 1 : kWaves;
+  r.units = r.token_units + (r.align > 1 ? (r.experts + wpt - 1) / wpt : 0);
+  if (!r.units) return hipSuccess;
+  const uint32_t blocks = blocks_for(r.units * wpt);
+  if (dtype == HC_F32) {
+    if (wpt == 1)
+      combine_grad_kernel<F32, 1><<<blocks, kThreads, 0, stream>>>(r);
+    else
+      combine_grad_kernel<F32, kWaves><<<blocks, kThreads, 0, stream>>>(r);
+  } else {
+    if (wpt == 1)
+      combine_grad_kernel<BF16, 1><<<blocks, kThreads, 0, stream>>>(r);
+    else
+      combine_grad_kernel<BF16, kWaves><<<blocks, kThreads, 0, stream>>>(r);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace hc

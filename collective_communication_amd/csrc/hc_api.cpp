@@ -116,15 +116,13 @@ void log_line(const char* fmt, ...) {
   fprintf(stderr, "hc: %s\n", buf);
 }
 
-}  // namespace hc
-
 namespace {
-
-using hc::Tap;
-
 thread_local std::string g_last_error;
+}
 
-hc_status_t fail(hc_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+const char* last_error() { return g_last_error.c_str(); }
+void clear_error() { g_last_error.clear(); }
+
 hc_status_t fail(hc_status_t st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -138,6 +136,14 @@ hc_status_t fail(hc_status_t st, const char* fmt, ...) {
 hc_status_t device_fail(hipError_t e, const char* where) {
   return fail(HC_ERR_DEVICE, "%s: %s", where, hipGetErrorString(e));
 }
+
+}  // namespace hc
+
+namespace {
+
+using hc::Tap;
+using hc::device_fail;
+using hc::fail;
 
 size_t esize(hc_dtype_t d) { return d == HC_F32 ? 4 : 2; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -562,7 +568,7 @@ const char* hc_status_string(hc_status_t s) {
   return "unknown status";
 }
 
-const char* hc_last_error(void) { return g_last_error.c_str(); }
+const char* hc_last_error(void) { return hc::last_error(); }
 
 int hc_copy_engine_available(void) { return dma_copies_offload() ? 1 : 0; }
 const char* hc_version(void) { return "hc 0.1 gfx950"; }
@@ -598,7 +604,7 @@ size_t hc_ring_tasks(int nranks, size_t count, size_t chunk, hc_task_t* tasks, s
 
 hc_status_t hc_allreduce(void* const* sendbufs, void* const* recvbufs, size_t count,
                          hc_dtype_t dtype, int nranks, const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, dtype, opts);
   if (st) return st;
   if (count == 0) return HC_SUCCESS;
@@ -633,7 +639,7 @@ hc_status_t hc_allreduce(void* const* sendbufs, void* const* recvbufs, size_t co
 
 hc_status_t hc_allreduce_bf16_f32carry(void* const* sendbufs, void* const* recvbufs, size_t count, int nranks,
                                        void* d_ws, size_t ws_bytes, const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, HC_BF16, opts);
   if (st) return st;
   if (count == 0) return HC_SUCCESS;
@@ -671,7 +677,7 @@ hc_status_t hc_allreduce_bf16_f32carry(void* const* sendbufs, void* const* recvb
 
 hc_status_t hc_allreduce_sgd(void* const* grads, void* const* weights, size_t count, hc_dtype_t dtype,
                              int nranks, float lr, const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, dtype, opts);
   if (st) return st;
   if (!(lr == lr) || lr == INFINITY || lr == -INFINITY)
@@ -737,7 +743,7 @@ size_t hc_workspace_bytes(hc_op_t op, size_t count, int nranks, hc_dtype_t dtype
 hc_status_t hc_reduce_scatter(void* const* sendbufs, void* const* recvbufs, size_t recvcount,
                               hc_dtype_t dtype, int nranks, void* d_ws, size_t ws_bytes,
                               const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, dtype, opts);
   if (st) return st;
   if (recvcount == 0) return HC_SUCCESS;
@@ -792,7 +798,7 @@ hc_status_t hc_reduce_scatter(void* const* sendbufs, void* const* recvbufs, size
 
 hc_status_t hc_all_gather(void* const* sendbufs, void* const* recvbufs, size_t sendcount,
                           hc_dtype_t dtype, int nranks, const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, dtype, opts);
   if (st) return st;
   if (sendcount == 0) return HC_SUCCESS;
@@ -858,7 +864,7 @@ enum class Coder { kPerBlock, kScoped, kEntropy, kStaged };
 hc_status_t compress_common(const uint16_t* d_in, size_t n, void* d_out, size_t out_cap, uint64_t* d_out_bytes,
                             void* d_ws, size_t ws_bytes, Coder coder, size_t table_blocks, hipStream_t stream) {
   const bool scoped = coder == Coder::kScoped;
-  g_last_error.clear();
+  hc::clear_error();
   if (!d_out || !d_out_bytes || !d_ws || (n && !d_in))
     return fail(HC_ERR_INVALID_ARGUMENT, "NULL pointer argument");
   if ((d_in && !aligned16(d_in)) || !aligned16(d_out) || !aligned16(d_ws) || ((uintptr_t)d_out_bytes & 7u))
@@ -899,7 +905,7 @@ hc_status_t hc_compress_bf16(const uint16_t* d_in, size_t n, void* d_out, size_t
 
 hc_status_t hc_compress_bf16_noalloc(const uint16_t* d_in, size_t n, void* d_out, size_t out_cap,
                                      uint64_t* d_out_bytes, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   if (n > hc::kNoAllocMaxBlocks * (size_t)HC_BLOCK_ELEMS)
     return fail(HC_ERR_INSUFFICIENT_CAPACITY, "n %zu exceeds the static scratch's %zu elements", n,
                 hc::kNoAllocMaxBlocks * (size_t)HC_BLOCK_ELEMS);
@@ -941,7 +947,7 @@ namespace {
 
 hc_status_t decompress_common(const void* d_in, size_t in_bytes, uint16_t* d_out, size_t n, int32_t* d_status,
                               bool entropy, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   if (!d_in || !d_status || (n && !d_out)) return fail(HC_ERR_INVALID_ARGUMENT, "NULL pointer argument");
   if (!aligned16(d_in) || (d_out && !aligned16(d_out)) || ((uintptr_t)d_status & 3u))
     return fail(HC_ERR_INVALID_ARGUMENT, "misaligned pointer argument");
@@ -971,7 +977,7 @@ hc_status_t hc_decompress_bf16_entropy(const void* d_in, size_t in_bytes, uint16
 hc_status_t hc_compressed_allreduce(void* const* sendbufs, void* const* recvbufs, size_t count,
                                     int nranks, void* d_ws, size_t ws_bytes, uint64_t* d_wire_bytes,
                                     const hc_opts_t* opts, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hc_status_t st = check_common(nranks, HC_BF16, opts);
   if (st) return st;
   if (opts && opts->cu_budget != 0)
@@ -1015,7 +1021,7 @@ hc_status_t hc_compressed_allreduce(void* const* sendbufs, void* const* recvbufs
 }
 
 hc_status_t hc_stream_create_cu_range(int first, int k, hipStream_t* out) {
-  g_last_error.clear();
+  hc::clear_error();
   if (!out) return fail(HC_ERR_INVALID_ARGUMENT, "out is NULL");
   if (k < 1) return fail(HC_ERR_INVALID_ARGUMENT, "k %d < 1", k);
   if (first < 0) return fail(HC_ERR_INVALID_ARGUMENT, "first %d < 0", first);
@@ -1040,7 +1046,7 @@ hc_status_t hc_stream_create_cu_range(int first, int k, hipStream_t* out) {
 hc_status_t hc_stream_create_cu_budget(int k, hipStream_t* out) { return hc_stream_create_cu_range(0, k, out); }
 
 hc_status_t hc_cu_census(uint32_t* d_ids, int n_workgroups, int hold_us, hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   if (!d_ids) return fail(HC_ERR_INVALID_ARGUMENT, "d_ids is NULL");
   if ((uintptr_t)d_ids & 3u) return fail(HC_ERR_INVALID_ARGUMENT, "d_ids is not 4-byte aligned");
   if (n_workgroups < 1 || n_workgroups > 65536)
@@ -1051,7 +1057,7 @@ hc_status_t hc_cu_census(uint32_t* d_ids, int n_workgroups, int hold_us, hipStre
 }
 
 hc_status_t hc_stream_destroy(hipStream_t stream) {
-  g_last_error.clear();
+  hc::clear_error();
   hipError_t e = hipStreamDestroy(stream);
   return e == hipSuccess ? HC_SUCCESS : device_fail(e, "hipStreamDestroy");
 }

@@ -1,0 +1,150 @@
+// key_sort.hpp -- a stable counting sort by one digit, shared by the tokens
+// of an embedding's gradient (one to four digits) and the slots of experts
+// (one digit).
+//
+// The input is cut into at most kMaxTiles tiles, one per workgroup of 16
+// waves.  A histogram launch counts each tile's digits; the scatter launch's
+// workgroups then add up the counts of the tiles before theirs themselves
+// (at most 64 x 1024 words out of the cache), so the pair needs no scan launch
+// between them.  Within a tile each wave owns a contiguous run of items: it
+// counts its run, the waves' counts are scanned per digit, and the wave walks
+// its run 64 items at a time, ranking equal digits by ballots.  Nothing
+// depends on the order in which atomics arrive.
+#pragma once
+
+#include "rows.hpp"
+#include "step_launch.hpp"
+
+namespace hc {
+
+constexpr uint32_t kSortThreads = 1024;
+constexpr uint32_t kSortWaves = kSortThreads / 64;
+constexpr uint32_t kMaxRadix = 1024;
+constexpr uint32_t kMaxTiles = 64;
+constexpr uint32_t kMinTile = 1024;     // items
+
+// Items per tile, a multiple of 1024 (64 per wave), for at most kMaxTiles tiles.
+inline uint32_t sort_tile(size_t n) {
+  const size_t per = (n + kMaxTiles - 1) / kMaxTiles;
+  const size_t t = (per + kMinTile - 1) / kMinTile * kMinTile;
+  return (uint32_t)(t < kMinTile ? kMinTile : t);
+}
+inline uint32_t sort_tiles(size_t n) { return (uint32_t)((n + sort_tile(n) - 1) / sort_tile(n)); }
+
+__device__ __forceinline__ uint32_t load_key(const KeySource& s, size_t i) {
+  const int64_t id = s.id_bytes == 8 ? static_cast<const int64_t*>(s.ids)[i] : (int64_t)static_cast<const int32_t*>(s.ids)[i];
+  // unsigned wrap-around: an id below start becomes a huge difference
+  const uint64_t k = (uint64_t)id - (uint64_t)s.start;
+  if (k >= s.nkeys || (s.use_skip && id == s.skip)) return kNoKey;
+  return (uint32_t)k;
+}
+
+// The lanes of the wave with this lane's digit, among those with `valid`.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid, uint32_t bits) {
+  uint64_t m = __ballot(valid);
+  for (uint32_t b = 0; b < bits; ++b) {
+    const uint64_t s = __ballot((digit >> b) & 1u);
+    m &= ((digit >> b) & 1u) ? s : ~s;
+  }
+  return m;
+}
+
+// Exclusive scan over the workgroup's kSortThreads values; *total: their sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* lds /* kSortWaves + 1 */, uint32_t* total) {
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(x, d);
+    if (lane_id() >= (uint32_t)d) x += y;
+  }
+  if (lane_id() == 63) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (uint32_t w = 0; w < kSortWaves; ++w) {
+    if (w < (threadIdx.x >> 6)) before += lds[w];
+    all += lds[w];
+  }
+  *total = all;
+  __syncthreads();
+  return before + x - v;
+}
+
+// One tile's histogram of digit(i) in [0, radix) over items [lo, hi);
+// kNoKey counts nowhere.
+template <typename Digit>
+__device__ __forceinline__ void tile_histogram(uint32_t* lds, uint32_t radix, size_t lo, size_t hi, Digit digit,
+                                               uint32_t* out) {
+  for (uint32_t d = threadIdx.x; d < radix; d += kSortThreads) lds[d] = 0;
+  __syncthreads();
+  for (size_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+    const uint32_t d = digit(i);
+    if (d != kNoKey) atomicAdd(&lds[d], 1u);
+  }
+  __syncthreads();
+  for (uint32_t d = threadIdx.x; d < radix; d += kSortThreads) out[d] = lds[d];
+}
+
+// Per digit: the sum of the tiles' counts before `tile`, and over all tiles.
+__device__ __forceinline__ void tile_sums(const uint32_t* hist, uint32_t radix, uint32_t tiles, uint32_t tile,
+                                          uint32_t d, uint32_t* before, uint32_t* total) {
+  uint32_t b = 0, a = 0;
+  if (d < radix) {
+#pragma unroll 8
+    for (uint32_t t = 0; t < tiles; ++t) {
+      const uint32_t c = hist[(size_t)t * radix + d];
+      b += t < tile ? c : 0;
+      a += c;
+    }
+  }
+  *before = b;
+  *total = a;
+}
+
+// Hands each item of [lo, hi) its place: put(i, digit, place) with place =
+// base(its digit) + how many items of the tile before it have the same digit.
+// counts: kSortWaves x radix words of LDS; base(d): the digit's first place
+// for this tile, called once by thread d.  Items without a key: put(i, kNoKey, 0).
+template <typename Digit, typename Put>
+__device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, uint32_t bits, size_t lo, size_t hi,
+                                            uint32_t tile_items, uint32_t my_base, Digit digit, Put put) {
+  const uint32_t w = wave_id(), lane = lane_id();
+  uint32_t* mine = counts + (size_t)w * radix;
+  for (uint32_t d = threadIdx.x; d < radix * kSortWaves; d += kSortThreads) counts[d] = 0;
+  __syncthreads();
+  const uint32_t run = tile_items / kSortWaves;
+  const size_t a = lo + (size_t)w * run;
+  const size_t b = a + run < hi ? a + run : hi;
+  for (size_t i = a + lane; i < b; i += 64) {
+    const uint32_t d = digit(i);
+    if (d != kNoKey) atomicAdd(&mine[d], 1u);
+  }
+  __syncthreads();
+  if (threadIdx.x < radix) {
+    uint32_t p = my_base;
+#pragma unroll
+    for (uint32_t v = 0; v < kSortWaves; ++v) {
+      const uint32_t c = counts[(size_t)v * radix + threadIdx.x];
+      counts[(size_t)v * radix + threadIdx.x] = p;
+      p += c;
+    }
+  }
+  __syncthreads();
+  for (size_t i0 = a; i0 < b; i0 += 64) {
+    const size_t i = i0 + lane;
+    const bool in = i < b;
+    const uint32_t d = in ? digit(i) : kNoKey;
+    const bool valid = d != kNoKey;
+    const uint64_t same = same_digit(d, valid, bits);
+    uint32_t place = 0;
+    if (valid) place = mine[d] + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+    // the counters are the wave's own: its lanes read before its lanes write
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (valid && (same >> lane) == 1) mine[d] = place + 1;   // the digit's last lane
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (in) put(i, d, place);
+  }
+}
+
+}  // namespace hc

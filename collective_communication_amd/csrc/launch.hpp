@@ -60,6 +60,13 @@ constexpr int kWgPerCuBudget = 8;   // workgroups per CU of a CU-budget grid
 bool log_enabled();
 void log_line(const char* fmt, ...) __attribute__((format(printf, 1, 2)));
 
+// Every entry point's error returns: the message becomes this thread's
+// hc_last_error() and the status is handed back.
+hc_status_t fail(hc_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+hc_status_t device_fail(hipError_t e, const char* where);
+const char* last_error();
+void clear_error();
+
 hipError_t launch_reduce_step(const Seg* segs, int nseg, hc_dtype_t dtype, int cu_budget,
                               hipStream_t stream);
 hipError_t launch_copy_step(const Seg* segs, int nseg, size_t elem_bytes, int cu_budget,

@@ -529,6 +529,153 @@ size_t hc_ring_tasks(int nranks, size_t count, size_t chunk, hc_task_t *tasks, s
  * HC_ERR_UNSUPPORTED. */
 int hc_copy_engine_available(void);
 
+/* ------------------------------------------------------------------------
+ * The training step around the exchange: what produces the gradients that
+ * the ranks sum, and what happens to the sum before the update.
+ *
+ * All of these are asynchronous on `stream`, may be captured into a graph,
+ * and give the same bits on every run: every sum has a fixed order.  Elements
+ * are fp32 or bf16; bf16 is widened exactly, sums are held in fp32 (the norm
+ * in fp64) and each result is rounded once, to nearest even.  Pointers need
+ * only their element's alignment, except workspaces (16 bytes); rows may be
+ * further apart than they are wide (strides in elements, never less than the
+ * width).  Offsets are 64-bit.  Outputs must not overlap inputs unless a call
+ * says so; that is the caller's to keep, like the sizes of its buffers.
+ * A workspace too small is HC_ERR_INSUFFICIENT_CAPACITY; its contents need
+ * not be kept between calls, and a call in flight owns it.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    HC_NORM_L2 = 0,    /* sqrt of the sum of squares */
+    HC_NORM_INF = 1,   /* largest absolute value */
+    HC_NORM_RANGE_MIN_ = INT32_MIN,
+    HC_NORM_RANGE_MAX_ = INT32_MAX
+} hc_norm_t;
+
+/*
+ * The norm of many gradients taken as one vector, and clipping by it.
+ *   grads, outs, counts, dtypes: HOST arrays of ntensors entries.  A tensor
+ *     of count 0 is skipped (its pointer may be NULL); ntensors 0 has norm 0.
+ *   hc_grad_norm: *d_norm (device fp32) = the norm.  Squares and sums are
+ *     fp64, so that no finite fp32 or bf16 gradient overflows or vanishes in
+ *     them; the result is rounded once to fp32.  A NaN anywhere gives NaN.
+ *   hc_clip_grads: outs[i] = coef * grads[i] with coef = min(1, max_norm /
+ *     (*d_norm + 1e-6)) in fp32 (NaN stays NaN, an infinite norm gives 0).
+ *     In place where outs[i] == grads[i]; a coefficient of 1 writes nothing
+ *     in place.  outs must not overlap one another or, unless equal, a
+ *     gradient (HC_ERR_INVALID_ARGUMENT): a gradient listed twice would be
+ *     scaled twice.  *d_norm may be a norm summed over more than these
+ *     tensors (other ranks' shards).
+ *   hc_clip_grad_norm: both, with *d_norm written.  max_norm >= 0.
+ *   ws: hc_grad_norm_workspace_bytes(ntensors) bytes (all three).
+ */
+size_t hc_grad_norm_workspace_bytes(size_t ntensors);
+hc_status_t hc_grad_norm(const void *const *grads, const size_t *counts, const hc_dtype_t *dtypes,
+                         size_t ntensors, hc_norm_t norm, float *d_norm, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+hc_status_t hc_clip_grads(const void *const *grads, void *const *outs, const size_t *counts,
+                          const hc_dtype_t *dtypes, size_t ntensors, const float *d_norm, float max_norm,
+                          void *ws, size_t ws_bytes, hipStream_t stream);
+hc_status_t hc_clip_grad_norm(const void *const *grads, void *const *outs, const size_t *counts,
+                              const hc_dtype_t *dtypes, size_t ntensors, hc_norm_t norm, float max_norm,
+                              float *d_norm, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * hc_embedding -- rows of a table by token id, scaled:
+ *   out[t] = round(scale * weight[ids[t] - vocab_start]).
+ * An id outside [vocab_start, vocab_start + vocab) gives a zero row: with the
+ * vocabulary split over ranks, each rank looks up its part and hc_allreduce
+ * adds the ranks' rows.
+ *   ids: ntokens device integers of id_bytes (4 or 8) bytes.
+ *   weight: vocab rows of dim elements, weight_stride elements apart; out:
+ *   ntokens rows, out_stride apart, of the same dtype.
+ *   vocab, ntokens < 2^31; dim < 2^31.
+ */
+hc_status_t hc_embedding(const void *ids, int id_bytes, size_t ntokens, const void *weight, hc_dtype_t dtype,
+                         size_t vocab, size_t dim, size_t weight_stride, int64_t vocab_start, float scale,
+                         void *out, size_t out_stride, hipStream_t stream);
+
+/*
+ * hc_embedding_grad -- the table's gradient, from tokens sorted by id:
+ *   dweight[v] = round(scale * sum over t with ids[t] - vocab_start == v of dout[t])
+ * summed in fp32 in an order that only the ids fix.  Rows that no token has
+ * become zero, or with accumulate != 0 stay as they are, while the others get
+ * dweight[v] + that sum (added in fp32, rounded once).
+ *   padding_id: tokens of this id (counted as in ids, before vocab_start) add
+ *     nothing; a negative value names none.
+ *   dout: ntokens rows of dout_dtype, dout_stride apart; dweight: vocab rows
+ *     of dweight_dtype, dweight_stride apart.
+ *   ws: hc_embedding_grad_workspace_bytes(ntokens, vocab, dim) bytes.
+ */
+size_t hc_embedding_grad_workspace_bytes(size_t ntokens, size_t vocab, size_t dim);
+hc_status_t hc_embedding_grad(const void *ids, int id_bytes, size_t ntokens, const void *dout,
+                              hc_dtype_t dout_dtype, size_t dout_stride, size_t vocab, size_t dim,
+                              int64_t vocab_start, int64_t padding_id, float scale, void *dweight,
+                              hc_dtype_t dweight_dtype, size_t dweight_stride, int accumulate, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Tokens sorted by expert, and back: the two sides of an expert-parallel
+ * exchange.  Token t chooses k experts; its choice j is slot s = t * k + j.
+ * Slots are laid out by expert, in slot order within an expert (stable), each
+ * expert's rows beginning at a multiple of row_align (1: packed).
+ *
+ * hc_expert_plan_t holds the layout.  The caller fills in the sizes and the
+ * device buffers; hc_expert_sort writes the buffers, the other calls read
+ * them:
+ *   row_of_slot[ntokens * k]: the slot's row, or -1 if its expert is not one
+ *     of these (another rank's, or a masked token's id).
+ *   slot_of_row[rows]: the row's slot, or -1 (padding, and every row past
+ *     the last expert's).
+ *   expert_offsets[nexperts + 1]: each expert's first row; the last entry is
+ *     the end of all rows in use, padding included.
+ *   expert_counts[nexperts]: each expert's slots.
+ *   rows: the rows the buffers have room for, at least
+ *     hc_expert_rows_bound(ntokens, k, nexperts, row_align).
+ * k in 1..HC_MAX_TOPK, nexperts in 1..HC_MAX_EXPERTS, row_align >= 1; slots
+ * and rows < 2^31.
+ */
+#define HC_MAX_TOPK 64
+#define HC_MAX_EXPERTS 1024
+typedef struct {
+    size_t ntokens;
+    int32_t k;
+    int32_t nexperts;
+    int32_t row_align;
+    size_t rows;
+    int32_t *row_of_slot;
+    int32_t *slot_of_row;
+    int32_t *expert_offsets;
+    int32_t *expert_counts;
+} hc_expert_plan_t;
+
+/* ntokens * k + min(nexperts, ntokens * k) * (row_align - 1); 0 on invalid sizes. */
+size_t hc_expert_rows_bound(size_t ntokens, int k, int nexperts, int row_align);
+size_t hc_expert_sort_workspace_bytes(size_t nslots, int nexperts);
+/* experts: ntokens * k device integers of id_bytes (4 or 8) bytes; this
+ * rank's experts are [expert_start, expert_start + nexperts). */
+hc_status_t hc_expert_sort(const void *experts, int id_bytes, int64_t expert_start, const hc_expert_plan_t *plan,
+                           void *ws, size_t ws_bytes, hipStream_t stream);
+/* rows[row_of_slot[t * k + j]] = x[t]; padding rows of an expert become zero,
+ * rows past the last expert's stay as they are. */
+hc_status_t hc_expert_dispatch(const void *x, hc_dtype_t dtype, size_t dim, size_t x_stride,
+                               const hc_expert_plan_t *plan, void *rows, size_t rows_stride, hipStream_t stream);
+/* out[t] = round(sum over j of weights[t * k + j] * rows[row_of_slot[t * k + j]]),
+ * in fp32, j ascending; a slot without a row adds nothing, so a token without
+ * any gets a zero row.  weights: ntokens * k device fp32, or NULL for ones
+ * (which makes it the gradient of hc_expert_dispatch). */
+hc_status_t hc_expert_combine(const void *rows, hc_dtype_t dtype, size_t dim, size_t rows_stride,
+                              const hc_expert_plan_t *plan, const float *weights, void *out, size_t out_stride,
+                              hipStream_t stream);
+/* The gradient of hc_expert_combine:
+ *   drows[row_of_slot[t * k + j]] = round(weights[t * k + j] * dout[t]), padding rows zero;
+ *   dweights[t * k + j] = sum over d of dout[t][d] * rows[row_of_slot[t * k + j]][d] in fp32,
+ *   0 for a slot without a row. */
+hc_status_t hc_expert_combine_grad(const void *dout, hc_dtype_t dtype, size_t dim, size_t dout_stride,
+                                   const void *rows, size_t rows_stride, const hc_expert_plan_t *plan,
+                                   const float *weights, void *drows, size_t drows_stride, float *dweights,
+                                   hipStream_t stream);
+
 const char *hc_status_string(hc_status_t status);
 const char *hc_last_error(void);  /* thread-local, "" when none */
 const char *hc_version(void);
