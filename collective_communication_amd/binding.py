@@ -493,46 +493,34 @@ def hc_compressed_allreduce(sendbufs, recvbufs, count: int | None, ws: torch.Ten
                                      _opts(chunk_fraction, 0, step_events), _stream_handle(stream)))
 
 
-# ----------------------------------------------------------------------------- gradients
+# ----------------------------------------------------------------------------- around the exchange
+#
+# These take their tensors to the C ABI through the module _native (see
+# csrc/native_binding.cpp), which checks them: TypeError for a dtype, ValueError
+# for anything else that does not fit.
 
 _NORMS = {"l2": HC_NORM_L2, "inf": HC_NORM_INF}
+_native = None
 
 
-def _tensor_list(tensors, name: str):
-    """Addresses, element counts and dtypes of many device tensors.  Each must
-    be dense (any order of its dimensions), since a norm and a scaling go over
-    its storage."""
-    n = len(tensors)
-    ptrs, counts, dtypes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)(), (ctypes.c_int32 * n)()
-    for i, t in enumerate(tensors):
-        if not t.is_cuda:
-            raise ValueError(f"{name}[{i}] is not a device tensor")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{name}[{i}] is not dense (strides {t.stride()} for shape {tuple(t.shape)})")
-        ptrs[i] = t.data_ptr()
-        counts[i] = t.numel()
-        dtypes[i] = _dtype(t)
-    return ptrs, counts, dtypes
+def _load_native():
+    global _native
+    load()
+    from . import _native as module
+
+    _native = module
+    return module
+
+
+def _raw_stream(stream):
+    """None (torch's current stream) and raw handles as they are."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _dense(t: torch.Tensor) -> bool:
-    want = 1
-    for st, size in sorted((st, size) for st, size in zip(t.stride(), t.shape) if size != 1):
-        if st != want:
-            return False
-        want *= size
-    return True
-
-
-def _outs(grads, outs):
-    if outs is None:
-        return grads
-    if len(outs) != len(grads):
-        raise ValueError("one output per gradient")
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride():
-            raise ValueError(f"outs[{i}] must have the dtype, shape and strides of grads[{i}]")
-    return outs
+    """True when the tensor's elements fill its storage without gaps, in any
+    order of its dimensions."""
+    return (_native or _load_native()).is_dense(t)
 
 
 def hc_grad_norm_workspace_bytes(ntensors: int) -> int:
@@ -541,83 +529,37 @@ def hc_grad_norm_workspace_bytes(ntensors: int) -> int:
 
 def hc_grad_norm(grads, d_norm: torch.Tensor, ws: torch.Tensor, *, norm: str = "l2", stream=None):
     """d_norm[0] = the norm of all grads as one vector ("l2" or "inf"); see
-    include/hc.h."""
-    L = load()
-    p, c, d = _tensor_list(grads, "grads")
-    np_ = _fptr(d_norm, 1, "d_norm")
-    _check(L.hc_grad_norm(p, c, d, len(grads), _NORMS[norm], np_, _dptr(ws, 1, "ws"), ws.numel() * ws.element_size(),
-                          _stream_handle(stream)))
+    include/hc.h.  Gradients may have any order of dimensions but no gaps."""
+    st = (_native or _load_native()).grad_norm(grads, d_norm, ws, _NORMS[norm], _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_clip_grads(grads, d_norm: torch.Tensor, max_norm: float, ws: torch.Tensor, *, outs=None, stream=None):
     """outs = grads * min(1, max_norm / (d_norm[0] + 1e-6)); in place when
     outs is None."""
-    L = load()
-    p, c, d = _tensor_list(grads, "grads")
-    o = p if outs is None else _tensor_list(_outs(grads, outs), "outs")[0]
-    np_ = _fptr(d_norm, 1, "d_norm")
-    _check(L.hc_clip_grads(p, o, c, d, len(grads), np_, float(max_norm), _dptr(ws, 1, "ws"),
-                           ws.numel() * ws.element_size(), _stream_handle(stream)))
+    st = (_native or _load_native()).clip_grads(grads, outs, d_norm, max_norm, ws, _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_clip_grad_norm(grads, max_norm: float, d_norm: torch.Tensor, ws: torch.Tensor, *, outs=None, norm: str = "l2",
                       stream=None):
     """hc_grad_norm and hc_clip_grads in one call; d_norm[0] receives the norm
     before clipping."""
-    L = load()
-    p, c, d = _tensor_list(grads, "grads")
-    o = p if outs is None else _tensor_list(_outs(grads, outs), "outs")[0]
-    np_ = _fptr(d_norm, 1, "d_norm")
-    _check(L.hc_clip_grad_norm(p, o, c, d, len(grads), _NORMS[norm], float(max_norm), np_, _dptr(ws, 1, "ws"),
-                               ws.numel() * ws.element_size(), _stream_handle(stream)))
-
-
-# ----------------------------------------------------------------------------- rows
-
-def _fptr(t: torch.Tensor, need: int, name: str) -> int:
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32")
-    return _dptr(t, 4 * need, name)
-
-
-def _ids(t: torch.Tensor, name: str):
-    if t.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"{name} must be int32 or int64")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous device tensor")
-    return t.data_ptr(), t.element_size(), t.numel()
-
-
-def _matrix(t: torch.Tensor, rows: int | None, dim: int | None, name: str):
-    """Address and row stride of a 2-D device tensor whose rows are dense."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D device tensor")
-    if rows is not None and t.shape[0] < rows or dim is not None and t.shape[1] != dim:
-        raise ValueError(f"{name} is {tuple(t.shape)}, needs ({rows}, {dim})")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if t.shape[1] > 1 and t.stride(1) != 1 or stride < t.shape[1]:
-        raise ValueError(f"{name} needs dense rows that do not overlap (strides {t.stride()})")
-    return t.data_ptr(), stride
-
-
-def _same_dtype(*tensors):
-    if any(t.dtype != tensors[0].dtype for t in tensors):
-        raise TypeError("all rows need one dtype")
-    return _dtype(tensors[0])
+    st = (_native or _load_native()).clip_grad_norm(grads, outs, _NORMS[norm], max_norm, d_norm, ws,
+                                                    _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_embedding(ids: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *, vocab_start: int = 0,
                  scale: float = 1.0, stream=None):
     """out[t] = scale * weight[ids[t] - vocab_start], zero for an id outside
     the table's range; see include/hc.h."""
-    L = load()
-    dt = _same_dtype(weight, out)
-    ip, ib, n = _ids(ids, "ids")
-    dim = weight.shape[-1]
-    wp, wst = _matrix(weight, None, dim, "weight")
-    op, ost = _matrix(out, n, dim, "out")
-    _check(L.hc_embedding(ip, ib, n, wp, dt, weight.shape[0], dim, wst, vocab_start, float(scale), op, ost,
-                          _stream_handle(stream)))
+    st = (_native or _load_native()).embedding(ids, weight, out, vocab_start, scale, _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_embedding_grad_workspace_bytes(ntokens: int, vocab: int, dim: int) -> int:
@@ -629,18 +571,12 @@ def hc_embedding_grad(ids: torch.Tensor, dout: torch.Tensor, dweight: torch.Tens
                       accumulate: bool = False, stream=None):
     """dweight[v] = scale * the sum of dout over the tokens with id
     vocab_start + v (added to dweight when accumulate); see include/hc.h."""
-    L = load()
-    ip, ib, n = _ids(ids, "ids")
-    dim = dweight.shape[-1]
-    dp, dst = _matrix(dout, n, dim, "dout")
-    wp, wst = _matrix(dweight, None, dim, "dweight")
-    _check(L.hc_embedding_grad(ip, ib, n, dp, _dtype(dout), dst, dweight.shape[0], dim, vocab_start,
-                               -1 if padding_id is None else padding_id, float(scale), wp, _dtype(dweight), wst,
-                               int(accumulate), _dptr(ws, 0, "ws"), ws.numel() * ws.element_size(),
-                               _stream_handle(stream)))
+    st = (_native or _load_native()).embedding_grad(ids, dout, dweight, ws, vocab_start,
+                                                    -1 if padding_id is None else padding_id, scale, accumulate,
+                                                    _raw_stream(stream))
+    if st:
+        _check(st)
 
-
-# ----------------------------------------------------------------------------- experts
 
 def hc_expert_rows_bound(ntokens: int, k: int, nexperts: int, row_align: int = 1) -> int:
     return int(load().hc_expert_rows_bound(ntokens, k, nexperts, row_align))
@@ -669,7 +605,7 @@ class ExpertPlan:
         self.rows = slot_of_row.numel()
         self._c = hc_expert_plan_t(ntokens, k, nexperts, row_align, self.rows, row_of_slot.data_ptr(),
                                    slot_of_row.data_ptr(), expert_offsets.data_ptr(), expert_counts.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        self._at = ctypes.addressof(self._c)
 
     @classmethod
     def for_sizes(cls, ntokens: int, k: int, nexperts: int, row_align: int = 1, device="cuda"):
@@ -682,50 +618,34 @@ def hc_expert_sort(experts: torch.Tensor, plan: ExpertPlan, ws: torch.Tensor | N
                    stream=None):
     """Lays the slots of experts (ntokens x k ids) out by expert in plan; ws:
     hc_expert_sort_workspace_bytes bytes, may be None where that is 0."""
-    L = load()
-    ip, ib, n = _ids(experts, "experts")
-    if n != plan.ntokens * plan.k:
-        raise ValueError(f"experts holds {n} ids, the plan {plan.ntokens} x {plan.k}")
-    wsp = _dptr(ws, 0, "ws") if ws is not None else None
-    _check(L.hc_expert_sort(ip, ib, expert_start, plan._ref, wsp, ws.numel() * ws.element_size() if ws is not None else 0,
-                            _stream_handle(stream)))
+    st = (_native or _load_native()).expert_sort(experts, plan._at, ws, expert_start, _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_expert_dispatch(x: torch.Tensor, plan: ExpertPlan, rows: torch.Tensor, *, stream=None):
     """rows[row_of_slot[t * k + j]] = x[t]; the experts' padding rows become zero."""
-    L = load()
-    dt = _same_dtype(x, rows)
-    dim = x.shape[-1]
-    xp, xst = _matrix(x, plan.ntokens, dim, "x")
-    rp, rst = _matrix(rows, plan.rows, dim, "rows")
-    _check(L.hc_expert_dispatch(xp, dt, dim, xst, plan._ref, rp, rst, _stream_handle(stream)))
+    st = (_native or _load_native()).expert_dispatch(x, plan._at, rows, _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_expert_combine(rows: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor | None, out: torch.Tensor, *,
                       stream=None):
     """out[t] = the sum over t's slots of weight * row (weights None: plain
     sum, the gradient of hc_expert_dispatch)."""
-    L = load()
-    dt = _same_dtype(rows, out)
-    dim = rows.shape[-1]
-    rp, rst = _matrix(rows, plan.rows, dim, "rows")
-    op, ost = _matrix(out, plan.ntokens, dim, "out")
-    wp = _fptr(weights, plan.ntokens * plan.k, "weights") if weights is not None else None
-    _check(L.hc_expert_combine(rp, dt, dim, rst, plan._ref, wp, op, ost, _stream_handle(stream)))
+    st = (_native or _load_native()).expert_combine(rows, plan._at, weights, out, _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 def hc_expert_combine_grad(dout: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor,
                            drows: torch.Tensor, dweights: torch.Tensor, *, stream=None):
     """The gradients of hc_expert_combine: drows by row, dweights by slot."""
-    L = load()
-    dt = _same_dtype(dout, rows, drows)
-    dim = rows.shape[-1]
-    dp, dst = _matrix(dout, plan.ntokens, dim, "dout")
-    rp, rst = _matrix(rows, plan.rows, dim, "rows")
-    gp, gst = _matrix(drows, plan.rows, dim, "drows")
-    wp = _fptr(weights, plan.ntokens * plan.k, "weights")
-    dwp = _fptr(dweights, plan.ntokens * plan.k, "dweights")
-    _check(L.hc_expert_combine_grad(dp, dt, dim, dst, rp, rst, plan._ref, wp, gp, gst, dwp, _stream_handle(stream)))
+    st = (_native or _load_native()).expert_combine_grad(dout, rows, plan._at, weights, drows, dweights,
+                                                         _raw_stream(stream))
+    if st:
+        _check(st)
 
 
 # ----------------------------------------------------------------------------- streams

@@ -4,7 +4,8 @@ Flags: -O3, -ffp-contract=off (no fused multiply-add contraction: every hop is
 one IEEE add), no fast-math, no flush-to-zero, packed-fp32 instructions
 disabled on the device (-Xclang -target-feature -Xclang -packed-fp32-ops).
 Objects go to _build/ at the repository root; the library lands next to this
-file so that it travels with the tree.  The two measurement programs of
+file so that it travels with the tree, and so does _native.so, the module that
+marshals torch tensors to it for calls where Python's share would be the larger.  The two measurement programs of
 measure/ at the repository root are built there: dma_contention (linked
 against libhc and rocBLAS from the system ROCm) and hbm_ceiling.
 """
@@ -21,11 +22,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhc.so")
+NATIVE = os.path.join(PKG, "_native.so")
 MEASURE = os.path.join(ROOT, "measure")
 DMA_TOOL = os.path.join(MEASURE, "dma_contention")
 CEILING_TOOL = os.path.join(MEASURE, "hbm_ceiling")
 ARCH = os.environ.get("HC_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["hc_api.cpp", "schedule.cpp", "ring_kernels.hip", "codec_kernels.hip", "car_chain.hip",
            "entropy_kernels.hip", "step_api.cpp", "grad_kernels.hip", "embed_kernels.hip", "expert_kernels.hip"]
@@ -45,17 +48,53 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_native() -> str:
+    """native_binding.cpp, host code against torch's and Python's headers."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "native_binding.cpp.o")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "native_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiler failed for native_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_native(obj: str):
+    """_native.so finds libhc.so beside it; torch's libraries are in the
+    process that imports it."""
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + ".tmp"
+    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", PKG, "-lhc", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
+    jobs = min(len(SOURCES) + 1, max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        native = ex.submit(_compile_native)
         objs = list(ex.map(_compile, SOURCES))
+        native_obj = native.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_native(native_obj)
     tmp = DMA_TOOL + ".tmp"
     cmd = [HIPCC, *COMMON, *DEVICE, "-x", "hip", os.path.join(MEASURE, "dma_contention.hip"), "-o", tmp,
            "-L", PKG, "-lhc", "-Wl,-rpath,$ORIGIN/../collective_communication_amd", "-L/opt/rocm/lib", "-lrocblas", "-Wl,-rpath,/opt/rocm/lib"]
@@ -70,7 +109,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hbm_ceiling build failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CEILING_TOOL)
     if verbose:
-        print(f"built {LIB}, {DMA_TOOL} and {CEILING_TOOL}")
+        print(f"built {LIB}, {NATIVE}, {DMA_TOOL} and {CEILING_TOOL}")
     return LIB
 
 
