@@ -26,11 +26,13 @@ constexpr uint32_t kChunkBytes = 16384;
 constexpr uint32_t kVecs = kChunkBytes / 16 / kThreads;   // 16-byte vectors per lane and chunk
 constexpr uint32_t kBatch = 128;        // tensors per kernel argument: 3.6 KB of the 4 KB
 constexpr uint32_t kMaxGrid = 2048;     // 8 workgroups of 4 waves on each of 256 CUs
+constexpr uint32_t kStreamChunks = (320u << 20) / kChunkBytes;
+constexpr uint32_t kFuseChunks = (128u << 20) / kChunkBytes;
 constexpr uint64_t kBf16Bit = 1ull << 63;
 
 struct Entry {
   const void* src;
-  void* dst;
+  void* dst;          // src where nothing is written
   uint64_t count;     // elements; kBf16Bit: bf16
 };
 struct Batch {
@@ -38,31 +40,75 @@ struct Batch {
   uint32_t first[kBatch];   // the first chunk of each tensor
 };
 
+// A chunk of a tensor begins where its output is 128-byte aligned (the first
+// begins up to a line before the tensor), so that a wave's stores fill whole
+// lines however the output lies; loads may straddle lines, stores must not:
+// with outputs at odd elements the clipping of 2^29 bf16 values took 385 us
+// on chunks counted from the tensor's start and takes 340 on these.
+__host__ __device__ __forceinline__ uint32_t lead_bytes(const void* p) { return (uint32_t)((uintptr_t)p & 127u); }
+__host__ __device__ __forceinline__ uint64_t chunks_of(const Entry& e) {
+  const uint64_t bytes = (e.count & ~kBf16Bit) * (e.count & kBf16Bit ? 2 : 4);
+  const uint32_t a = lead_bytes(e.src), b = lead_bytes(e.dst);
+  return (bytes + (a > b ? a : b) + kChunkBytes - 1) / kChunkBytes;
+}
+
 // The table in the workspace: entries, then first chunks.
 struct TableView {
   const Entry* e;
   const uint32_t* first;
 };
 
-__global__ void __launch_bounds__(kBatch) table_kernel(Batch b, uint32_t n, Entry* e, uint32_t* first) {
+// Up to kPacked tensors as a table launch's arguments, 18 bytes each: 48-bit
+// addresses, and the count and type in what is left over.
+constexpr uint32_t kPacked = 224;
+struct Packed {
+  uint64_t src[kPacked], dst[kPacked];    // bits 48..63: the count's bits 0..15 and 16..31
+  uint16_t rest[kPacked];                 // the count's bits 32..46; bit 15: bf16
+};
+
+// Writes a batch's entries and first chunks.
+__global__ void __launch_bounds__(kThreads) table_kernel(Packed b, uint32_t n, uint32_t first_chunk, Entry* e,
+                                                         uint32_t* first) {
+  __shared__ uint32_t lds[kWaves];
   const uint32_t i = threadIdx.x;
+  constexpr uint64_t kAddress = (1ull << 48) - 1;
+  Entry x = {nullptr, nullptr, 0};
   if (i < n) {
-    e[i] = b.e[i];
-    first[i] = b.first[i];
+    x.src = reinterpret_cast<const void*>(b.src[i] & kAddress);
+    x.dst = reinterpret_cast<void*>(b.dst[i] & kAddress);
+    x.count = (b.src[i] >> 48) | (b.dst[i] >> 48) << 16 | (uint64_t)(b.rest[i] & 0x7FFFu) << 32;
+    if (b.rest[i] & 0x8000u) x.count |= kBf16Bit;
+  }
+  const uint32_t mine = i < n ? (uint32_t)chunks_of(x) : 0;
+  uint32_t sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(sum, d);
+    if (lane_id() >= (uint32_t)d) sum += y;
+  }
+  if (lane_id() == 63) lds[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  uint32_t before = first_chunk;
+  for (uint32_t w = 0; w < (threadIdx.x >> 6); ++w) before += lds[w];
+  if (i < n) {
+    e[i] = x;
+    first[i] = before + sum - mine;
   }
 }
 
-// The tensor that holds chunk c: the last whose first chunk is not after it.
+// The tensor that holds chunk c, the last whose first chunk is not after it:
+// a search over 64 places at a time, one per lane, so two loads in turn find
+// it among 4096 tensors.  Every lane of the wave calls it.
 __device__ __forceinline__ uint32_t find(const uint32_t* first, uint32_t n, uint32_t c) {
-  uint32_t lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (first[mid] <= c)
-      lo = mid;
-    else
-      hi = mid;
+  uint32_t lo = 0;
+  while (n > 1) {
+    const uint32_t step = (n + 63) / 64, at = lane_id() * step;
+    const uint64_t not_after = __ballot(at < n && first[lo + at] <= c);
+    const uint32_t skip = ((uint32_t)__popcll(not_after) - 1) * step;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
   }
-  return lo;
+  return first_lane_read(lo);
 }
 
 template <bool INF>
@@ -107,22 +153,47 @@ __device__ __forceinline__ void add_vec(vec4 v, double* acc, uint32_t& big) {
   }
 }
 
-template <typename T, bool INF>
-__device__ __forceinline__ void norm_chunk(const void* src, uint64_t at, uint64_t count, double* acc, uint32_t& big) {
-  constexpr uint32_t kElems = kChunkBytes / sizeof(typename T::raw);
-  const uint64_t left = count - at;
-  const typename T::raw* p = elem<T>(src, at);
-  if (left >= kElems) {
-    vec4 v[kVecs];
+// Where chunk c lies: its tensor, and its first byte there (negative where the
+// chunk begins before the tensor).  A full chunk lies inside the tensor whole.
+struct Place {
+  const void* src;
+  void* dst;
+  int64_t at, bytes;
+  bool bf16, full;
+};
+
+// OUT: counted from the output's line, else from the input's.
+template <bool OUT>
+__device__ __forceinline__ Place place_of(const Entry* e, const uint32_t* first, uint32_t n, uint32_t c) {
+  const uint32_t t = find(first, n, c);
+  const Entry x = e[t];
+  Place p;
+  p.src = x.src;
+  p.dst = x.dst;
+  p.bf16 = (x.count & kBf16Bit) != 0;
+  p.bytes = (int64_t)((x.count & ~kBf16Bit) << (p.bf16 ? 1 : 2));
+  p.at = (int64_t)(c - first[t]) * kChunkBytes - lead_bytes(OUT ? x.dst : x.src);
+  p.full = p.at >= 0 && p.at + kChunkBytes <= p.bytes;
+  return p;
+}
+
+template <bool NT>
+__device__ __forceinline__ void load_full(const Place& p, vec4* v) {
+  const char* q = static_cast<const char*>(p.src) + p.at + threadIdx.x * 16;
 #pragma unroll
-    for (uint32_t u = 0; u < kVecs; ++u)
-      v[u] = *reinterpret_cast<const vec4_u*>(p + (size_t)(u * kThreads + threadIdx.x) * T::kVec);
-#pragma unroll
-    for (uint32_t u = 0; u < kVecs; ++u) add_vec<T, INF>(v[u], acc, big);
-  } else {
-    for (uint32_t i = threadIdx.x * T::kVec; i < left; i += kThreads * T::kVec)
-      add_vec<T, INF>(load_vec<T>(p + i, (uint32_t)left - i), acc, big);
+  for (uint32_t u = 0; u < kVecs; ++u) {
+    const vec4_u* w = reinterpret_cast<const vec4_u*>(q + u * kThreads * 16);
+    v[u] = NT ? __builtin_nontemporal_load(w) : *w;
   }
+}
+
+// A chunk that its tensor's ends cut: fn(element, how many are left) per vector.
+template <typename T, typename Fn>
+__device__ __forceinline__ void each_vec(const Place& p, Fn fn) {
+  constexpr int64_t kSize = sizeof(typename T::raw);
+  const int64_t lo = p.at < 0 ? 0 : p.at / kSize;
+  const int64_t end = p.at + kChunkBytes < p.bytes ? p.at + kChunkBytes : p.bytes, hi = end / kSize;
+  for (int64_t i = lo + threadIdx.x * T::kVec; i < hi; i += kThreads * T::kVec) fn((size_t)i, (uint32_t)(hi - i));
 }
 
 template <bool INF>
@@ -130,28 +201,40 @@ __device__ void norm_body(const Entry* e, const uint32_t* first, uint32_t n, uin
   __shared__ double lds[kWaves];
   double acc[4] = {0, 0, 0, 0};
   uint32_t big = 0;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const uint32_t t = find(first, n, c);
-    const Entry x = e[t];
-    const uint64_t k = c - first[t];
-    if (x.count & kBf16Bit)
-      norm_chunk<BF16, INF>(x.src, k * (kChunkBytes / 2), x.count & ~kBf16Bit, acc, big);
-    else
-      norm_chunk<F32, INF>(x.src, k * (kChunkBytes / 4), x.count, acc, big);
+  uint32_t c = blockIdx.x;
+  Place p = place_of<false>(e, first, n, c);
+  for (;;) {
+    vec4 v[kVecs];
+    if (p.full) load_full<true>(p, v);
+    // the next chunk is looked up while this one's data are on their way
+    c += gridDim.x;
+    const bool more = c >= gridDim.x && c < chunks;
+    Place next = p;
+    if (more) next = place_of<false>(e, first, n, c);
+    __builtin_amdgcn_sched_barrier(0);
+    if (p.full) {
+      if (p.bf16) {
+#pragma unroll
+        for (uint32_t u = 0; u < kVecs; ++u) add_vec<BF16, INF>(v[u], acc, big);
+      } else {
+#pragma unroll
+        for (uint32_t u = 0; u < kVecs; ++u) add_vec<F32, INF>(v[u], acc, big);
+      }
+    } else if (p.bf16) {
+      each_vec<BF16>(p, [&](size_t i, uint32_t left) {
+        add_vec<BF16, INF>(load_vec<BF16>(elem<BF16>(p.src, i), left), acc, big);
+      });
+    } else {
+      each_vec<F32>(p, [&](size_t i, uint32_t left) {
+        add_vec<F32, INF>(load_vec<F32>(elem<F32>(p.src, i), left), acc, big);
+      });
+    }
+    if (!more) break;
+    p = next;
   }
   double v = INF ? (double)bits_f32(big) : (acc[0] + acc[1]) + (acc[2] + acc[3]);
   v = block_join<INF>(v, lds);
   if (threadIdx.x == 0) partials[blockIdx.x] = v;
-}
-
-template <bool INF>
-__global__ void __launch_bounds__(kThreads) norm_args_kernel(Batch b, uint32_t n, uint32_t chunks, double* partials) {
-  norm_body<INF>(b.e, b.first, n, chunks, partials);
-}
-template <bool INF>
-__global__ void __launch_bounds__(kThreads) norm_table_kernel(TableView t, uint32_t n, uint32_t chunks,
-                                                              double* partials) {
-  norm_body<INF>(t.e, t.first, n, chunks, partials);
 }
 
 // The norm from the workgroups' partials, the same bits in every workgroup.
@@ -165,6 +248,16 @@ __device__ __forceinline__ float norm_of(const double* partials, uint32_t n) {
 }
 
 template <bool INF>
+__global__ void __launch_bounds__(kThreads) norm_args_kernel(Batch b, uint32_t n, uint32_t chunks, double* partials) {
+  norm_body<INF>(b.e, b.first, n, chunks, partials);
+}
+template <bool INF>
+__global__ void __launch_bounds__(kThreads) norm_table_kernel(TableView t, uint32_t n, uint32_t chunks,
+                                                              double* partials) {
+  norm_body<INF>(t.e, t.first, n, chunks, partials);
+}
+
+template <bool INF>
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double* partials, uint32_t n, float* norm) {
   const float v = norm_of<INF>(partials, n);
   if (threadIdx.x == 0) *norm = v;
@@ -175,73 +268,75 @@ __device__ __forceinline__ float clip_coef(float norm, float max_norm) {
   return c > 1.0f ? 1.0f : c;   // NaN stays NaN
 }
 
-template <typename T>
-__device__ __forceinline__ void clip_chunk(const Entry& x, uint64_t at, uint64_t count, float coef) {
-  constexpr uint32_t kElems = kChunkBytes / sizeof(typename T::raw);
-  const uint64_t left = count - at;
-  const typename T::raw* p = elem<T>(x.src, at);
-  typename T::raw* q = elem<T>(x.dst, at);
-  if (left >= kElems) {
-    vec4 v[kVecs];
+template <typename T, bool NT>
+__device__ __forceinline__ void scale_full(const Place& p, const vec4* v, float coef) {
+  char* q = static_cast<char*>(p.dst) + p.at + threadIdx.x * 16;
 #pragma unroll
-    for (uint32_t u = 0; u < kVecs; ++u)
-      v[u] = *reinterpret_cast<const vec4_u*>(p + (size_t)(u * kThreads + threadIdx.x) * T::kVec);
+  for (uint32_t u = 0; u < kVecs; ++u) {
+    float f[T::kVec];
+    T::unpack(v[u], f);
 #pragma unroll
-    for (uint32_t u = 0; u < kVecs; ++u) {
-      float f[T::kVec];
-      T::unpack(v[u], f);
-#pragma unroll
-      for (int i = 0; i < T::kVec; ++i) f[i] *= coef;
-      *reinterpret_cast<vec4_u*>(q + (size_t)(u * kThreads + threadIdx.x) * T::kVec) = T::pack(f);
-    }
-  } else {
-    for (uint32_t i = threadIdx.x * T::kVec; i < left; i += kThreads * T::kVec) {
-      float f[T::kVec];
-      T::unpack(load_vec<T>(p + i, (uint32_t)left - i), f);
-#pragma unroll
-      for (int j = 0; j < T::kVec; ++j) f[j] *= coef;
-      store_vec<T>(q + i, T::pack(f), (uint32_t)left - i);
-    }
+    for (int i = 0; i < T::kVec; ++i) f[i] *= coef;
+    store_vec<T, NT>(reinterpret_cast<typename T::raw*>(q + u * kThreads * 16), T::pack(f), T::kVec);
   }
 }
+template <typename T>
+__device__ __forceinline__ void scale_cut(const Place& p, float coef) {
+  each_vec<T>(p, [&](size_t i, uint32_t left) {
+    float f[T::kVec];
+    T::unpack(load_vec<T>(elem<T>(p.src, i), left), f);
+#pragma unroll
+    for (int j = 0; j < T::kVec; ++j) f[j] *= coef;
+    store_vec<T>(elem<T>(p.dst, i), T::pack(f), left);
+  });
+}
 
-// Chunks from the last one down: the norm pass read those last, so they are
-// the ones the caches still hold.
-template <bool INF>
+template <bool INF, bool NT>
 __device__ void clip_body(const Entry* e, const uint32_t* first, uint32_t n, uint32_t chunks, const double* partials,
                           uint32_t npartials, float* norm, float max_norm) {
-  float v;
+  uint32_t c = blockIdx.x;
+  Place p = place_of<true>(e, first, n, c);
+  vec4 v[kVecs];
+  if (p.full) load_full<false>(p, v);     // on its way while the norm is added up
+  float total;
   if (partials) {
-    v = norm_of<INF>(partials, npartials);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    total = norm_of<INF>(partials, npartials);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   } else {
-    v = *norm;
+    total = *norm;
   }
-  const float coef = clip_coef(v, max_norm);
-  for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const uint32_t c = chunks - 1 - i;
-    const uint32_t t = find(first, n, c);
-    const Entry x = e[t];
-    if (coef == 1.0f && x.dst == x.src) continue;
-    const uint64_t k = c - first[t];
-    if (x.count & kBf16Bit)
-      clip_chunk<BF16>(x, k * (kChunkBytes / 2), x.count & ~kBf16Bit, coef);
-    else
-      clip_chunk<F32>(x, k * (kChunkBytes / 4), x.count, coef);
+  const float coef = clip_coef(total, max_norm);
+  for (;;) {
+    if (coef != 1.0f || p.dst != p.src) {
+      if (p.full) {
+        if (p.bf16)
+          scale_full<BF16, NT>(p, v, coef);
+        else
+          scale_full<F32, NT>(p, v, coef);
+      } else if (p.bf16) {
+        scale_cut<BF16>(p, coef);
+      } else {
+        scale_cut<F32>(p, coef);
+      }
+    }
+    c += gridDim.x;
+    if (c < gridDim.x || c >= chunks) break;
+    p = place_of<true>(e, first, n, c);
+    if (p.full) load_full<false>(p, v);
   }
 }
 
-template <bool INF>
+template <bool INF, bool NT>
 __global__ void __launch_bounds__(kThreads) clip_args_kernel(Batch b, uint32_t n, uint32_t chunks,
                                                              const double* partials, uint32_t npartials, float* norm,
                                                              float max_norm) {
-  clip_body<INF>(b.e, b.first, n, chunks, partials, npartials, norm, max_norm);
+  clip_body<INF, NT>(b.e, b.first, n, chunks, partials, npartials, norm, max_norm);
 }
-template <bool INF>
+template <bool INF, bool NT>
 __global__ void __launch_bounds__(kThreads) clip_table_kernel(TableView t, uint32_t n, uint32_t chunks,
                                                               const double* partials, uint32_t npartials, float* norm,
                                                               float max_norm) {
-  clip_body<INF>(t.e, t.first, n, chunks, partials, npartials, norm, max_norm);
+  clip_body<INF, NT>(t.e, t.first, n, chunks, partials, npartials, norm, max_norm);
 }
 
 // Workspace: kMaxGrid partials, then the table.
@@ -256,41 +351,72 @@ struct Plan {
   uint32_t n = 0, chunks = 0, grid = 0;
 };
 
+Entry entry_of(const void* const* grads, void* const* outs, const size_t* counts, const hc_dtype_t* dtypes, size_t i) {
+  return Entry{grads[i], outs ? outs[i] : const_cast<void*>(grads[i]),
+               (uint64_t)counts[i] | (dtypes[i] == HC_BF16 ? kBf16Bit : 0)};
+}
+
 hipError_t make_plan(const void* const* grads, void* const* outs, const size_t* counts, const hc_dtype_t* dtypes,
                      size_t ntensors, void* ws, hipStream_t stream, Plan* p) {
-  size_t live = 0;
   uint64_t chunks = 0;
   for (size_t i = 0; i < ntensors; ++i) {
-    const uint64_t elems = kChunkBytes / (dtypes[i] == HC_BF16 ? 2 : 4);
-    live += counts[i] != 0;
-    chunks += (counts[i] + elems - 1) / elems;
+    if (counts[i] == 0) continue;
+    const Entry x = entry_of(grads, outs, counts, dtypes, i);
+    if (((uintptr_t)x.src | (uintptr_t)x.dst) >> 48) return hipErrorInvalidValue;
+    ++p->n;
+    chunks += chunks_of(x);
     if (chunks > 0xFFFFFFFFull - kMaxGrid) return hipErrorInvalidValue;   // 64 TB of gradients
   }
-  p->by_args = live <= kBatch;
+  p->chunks = (uint32_t)chunks;
+  p->grid = p->chunks < kMaxGrid ? p->chunks : kMaxGrid;
+  p->by_args = p->n <= kBatch && p->chunks <= kMaxGrid;
   Entry* table = reinterpret_cast<Entry*>(static_cast<char*>(ws) + kPartialBytes);
-  uint32_t* firsts = reinterpret_cast<uint32_t*>(table + live);
-  uint32_t k = 0, done = 0;
-  chunks = 0;
+  uint32_t* firsts = reinterpret_cast<uint32_t*>(table + p->n);
+  p->view = TableView{table, firsts};
+  Packed pack;
+  uint32_t k = 0, done = 0, first = 0, next = 0;
   for (size_t i = 0; i < ntensors; ++i) {
     if (counts[i] == 0) continue;
-    const bool bf = dtypes[i] == HC_BF16;
-    p->batch.e[k] = Entry{grads[i], outs ? outs[i] : nullptr, (uint64_t)counts[i] | (bf ? kBf16Bit : 0)};
-    p->batch.first[k] = (uint32_t)chunks;
-    const uint64_t elems = kChunkBytes / (bf ? 2 : 4);
-    chunks += (counts[i] + elems - 1) / elems;
-    ++k;
-    ++p->n;
-    if (!p->by_args && (k == kBatch || p->n == live)) {
-      table_kernel<<<1, kBatch, 0, stream>>>(p->batch, k, table + done, firsts + done);
+    const Entry x = entry_of(grads, outs, counts, dtypes, i);
+    if (p->by_args) {
+      p->batch.e[k] = x;
+      p->batch.first[k++] = next;
+    } else {
+      const uint64_t c = counts[i];
+      pack.src[k] = (uint64_t)(uintptr_t)x.src | c << 48;
+      pack.dst[k] = (uint64_t)(uintptr_t)x.dst | (c >> 16) << 48;
+      pack.rest[k++] = (uint16_t)(c >> 32 | (dtypes[i] == HC_BF16 ? 0x8000u : 0));
+    }
+    next += (uint32_t)chunks_of(x);
+    if (!p->by_args && (k == kPacked || done + k == p->n)) {
+      table_kernel<<<1, kThreads, 0, stream>>>(pack, k, first, table + done, firsts + done);
       if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
       done += k;
+      first = next;
       k = 0;
     }
   }
-  p->view = TableView{table, firsts};
-  p->chunks = (uint32_t)chunks;
-  p->grid = p->chunks < kMaxGrid ? p->chunks : kMaxGrid;
   return hipSuccess;
+}
+
+// The clipping launch; partials NULL: the norm is in *norm already.
+template <bool INF>
+hipError_t run_clip(const Plan& p, float max_norm, float* norm, const double* partials, hipStream_t stream) {
+  const uint32_t grid = partials ? p.grid : p.chunks;
+  const uint32_t np = partials ? p.grid : 0;
+  const bool nt = p.chunks >= kStreamChunks;
+  if (p.by_args) {
+    if (nt)
+      clip_args_kernel<INF, true><<<grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials, np, norm, max_norm);
+    else
+      clip_args_kernel<INF, false><<<grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials, np, norm, max_norm);
+  } else {
+    if (nt)
+      clip_table_kernel<INF, true><<<grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials, np, norm, max_norm);
+    else
+      clip_table_kernel<INF, false><<<grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials, np, norm, max_norm);
+  }
+  return hipGetLastError();
 }
 
 template <bool INF>
@@ -302,13 +428,10 @@ hipError_t run(const Plan& p, bool clip, float max_norm, float* norm, double* pa
       norm_table_kernel<INF><<<p.grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (!clip || !p.grid)
-    finish_kernel<INF><<<1, kThreads, 0, stream>>>(partials, p.grid, norm);
-  else if (p.by_args)
-    clip_args_kernel<INF><<<p.grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials, p.grid, norm, max_norm);
-  else
-    clip_table_kernel<INF><<<p.grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials, p.grid, norm, max_norm);
-  return hipGetLastError();
+  if (clip && p.grid && p.chunks <= kFuseChunks) return run_clip<INF>(p, max_norm, norm, partials, stream);
+  finish_kernel<INF><<<1, kThreads, 0, stream>>>(partials, p.grid, norm);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  return clip && p.grid ? run_clip<INF>(p, max_norm, norm, nullptr, stream) : hipSuccess;
 }
 
 }  // namespace
@@ -331,12 +454,7 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const s
   Plan p;
   if (hipError_t e = make_plan(grads, outs, counts, dtypes, ntensors, ws, stream, &p); e != hipSuccess) return e;
   if (!p.grid) return hipSuccess;
-  float* norm = const_cast<float*>(d_norm);   // read only, without partials
-  if (p.by_args)
-    clip_args_kernel<false><<<p.grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, nullptr, 0, norm, max_norm);
-  else
-    clip_table_kernel<false><<<p.grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, nullptr, 0, norm, max_norm);
-  return hipGetLastError();
+  return run_clip<false>(p, max_norm, const_cast<float*>(d_norm), nullptr, stream);   // only read, without partials
 }
 
 }  // namespace hc

@@ -77,9 +77,12 @@ __device__ __forceinline__ typename T::raw* elem(void* p, size_t i) {
 
 // The vector at element p of a row with `left` (>= 1) elements from p on;
 // elements past the row's end read as zero and are not touched.
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ vec4 load_vec(const typename T::raw* p, uint32_t left) {
-  if (left >= T::kVec) return *reinterpret_cast<const vec4_u*>(p);
+  if (left >= T::kVec) {
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const vec4_u*>(p));
+    return *reinterpret_cast<const vec4_u*>(p);
+  }
   vec4 v = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < T::kVec; ++i)

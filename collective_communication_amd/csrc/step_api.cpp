@@ -70,7 +70,7 @@ hc_status_t check_tensors(const void* const* grads, const size_t* counts, const 
   for (size_t i = 0; i < n; ++i) {
     if (dtypes[i] != HC_F32 && dtypes[i] != HC_BF16)
       return fail(HC_ERR_INVALID_ARGUMENT, "dtypes[%zu]: unknown dtype %d", i, (int)dtypes[i]);
-    if (counts[i] > ((size_t)1 << 48)) return fail(HC_ERR_INVALID_ARGUMENT, "counts[%zu] = %zu", i, counts[i]);
+    if (counts[i] >= ((size_t)1 << 47)) return fail(HC_ERR_INVALID_ARGUMENT, "counts[%zu] = %zu", i, counts[i]);
     if (!counts[i]) continue;
     if (!grads[i]) return fail(HC_ERR_INVALID_ARGUMENT, "grads[%zu] is NULL", i);
     if ((uintptr_t)grads[i] % esize(dtypes[i]))
