@@ -29,7 +29,7 @@ inline uint32_t blocks_for(uint64_t waves) {
 
 // A wave handles 64 >> lg rows of 1 << lg vectors (lg < 6: narrow tables), or
 // a slice of U * 64 vectors of one row (lg == 6).
-template <typename T, int U>
+template <typename T, int U, bool NT>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size_t ntokens, const void* weight,
                                                              uint32_t dim, size_t wstride, float scale, void* out,
                                                              size_t ostride, uint32_t lg, uint32_t slices,
@@ -57,10 +57,44 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
       T::unpack(x[i], f);
 #pragma unroll
       for (int j = 0; j < T::kVec; ++j) f[j] *= scale;
-      store_vec<T>(elem<T>(out, t * ostride + (size_t)v * T::kVec), key == kNoKey ? vec4{0, 0, 0, 0} : T::pack(f),
+      store_vec<T, NT>(elem<T>(out, t * ostride + (size_t)v * T::kVec), key == kNoKey ? vec4{0, 0, 0, 0} : T::pack(f),
                    dim - v * T::kVec);
     }
   }
+}
+
+// ---------------------------------------------------------------- zeroing beside the sort
+
+// The sort's launches occupy a quarter of the GPU for a few microseconds each
+// and depend on nothing but the ids; the other compute units meanwhile zero
+// the first rows of the table, tokens or not (the sums come later and write
+// theirs again).  Pieces of some 64 KB: of one flat range where the rows are
+// contiguous, else whole rows.
+constexpr uint64_t kPieceBytes = 65536;
+
+struct ZeroJob {
+  char* base = nullptr;
+  uint64_t row_bytes = 0, stride = 0;   // flat: one row of all
+  uint64_t rows = 0, rows_per_piece = 0;
+  uint64_t pieces = 0, done = 0;
+  bool flat = false;
+};
+
+__device__ __forceinline__ void zero_span(char* p, uint64_t bytes, uint32_t lane, uint32_t lanes) {
+  for (uint64_t i = lane * 16; i < bytes; i += lanes * 16)
+    store_vec<BF16>(reinterpret_cast<uint16_t*>(p + i), vec4{0, 0, 0, 0},
+                    bytes - i < 16 ? (uint32_t)(bytes - i) / 2 : BF16::kVec);
+}
+
+__device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
+  if (z.flat) {
+    const uint64_t at = piece * kPieceBytes;
+    zero_span(z.base + at, z.row_bytes - at < kPieceBytes ? z.row_bytes - at : kPieceBytes, threadIdx.x, kSortThreads);
+    return;
+  }
+  const uint64_t r0 = piece * z.rows_per_piece;
+  for (uint64_t r = r0 + wave_id(); r < z.rows && r < r0 + z.rows_per_piece; r += kSortWaves)
+    zero_span(z.base + r * z.stride, z.row_bytes, lane_id(), 64);
 }
 
 // ---------------------------------------------------------------- sorting the ids
@@ -70,7 +104,12 @@ constexpr uint32_t kRankMax = 4096;     // ids sorted by counting smaller ones, 
 // Each workgroup places 64 ids: its 16 waves compare them with a sixteenth of
 // all ids each.  n^2 comparisons, 2 instructions each, beat the launches of a
 // radix sort while n is small.
-__global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint32_t n, uint32_t* keys, uint32_t* pos) {
+__global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint32_t n, uint32_t* keys, uint32_t* pos,
+                                                            uint32_t groups, ZeroJob zero) {
+  if (blockIdx.x >= groups) {
+    zero_piece(zero, zero.done + blockIdx.x - groups);
+    return;
+  }
   __shared__ __attribute__((aligned(16))) uint32_t all[kRankMax];
   __shared__ uint32_t part[kSortWaves][64];
   const uint32_t padded = (n + 63) & ~63u;
@@ -89,8 +128,15 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint3
     c += (k[0] < below) + (k[1] < below) + (k[2] < below) + (k[3] < below);
   };
   uint32_t j = lo;
+#pragma unroll 4
   for (; j < hi && j < g0; j += 4) count4(j, key + 1);          // earlier ids: equal ones come first
-  for (; j < hi && j < g0 + 64; ++j) c += all[j] < key + (j < i ? 1 : 0);
+#pragma unroll 4
+  for (; j < hi && j < g0 + 64; j += 4) {
+    const vec4 k = *reinterpret_cast<const vec4*>(&all[j]);
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) c += k[q] < key + (j + q < i ? 1 : 0);
+  }
+#pragma unroll 4
   for (; j < hi; j += 4) count4(j, key);                        // later ids
   part[threadIdx.x >> 6][lane_id()] = c;
   __syncthreads();
@@ -121,7 +167,11 @@ __device__ __forceinline__ uint32_t pass_digit(const Pass& p, size_t i) {
   return k == kNoKey ? kNoKey : (k >> p.shift) & ((1u << p.bits) - 1);
 }
 
-__global__ void __launch_bounds__(kSortThreads) pass_histogram_kernel(Pass p) {
+__global__ void __launch_bounds__(kSortThreads) pass_histogram_kernel(Pass p, ZeroJob zero) {
+  if (blockIdx.x >= p.tiles) {
+    zero_piece(zero, zero.done + blockIdx.x - p.tiles);
+    return;
+  }
   __shared__ uint32_t lds[kMaxRadix];
   const uint32_t radix = 1u << p.bits;
   const size_t lo = (size_t)blockIdx.x * p.tile;
@@ -129,16 +179,22 @@ __global__ void __launch_bounds__(kSortThreads) pass_histogram_kernel(Pass p) {
   tile_histogram(lds, radix, lo, hi, [&](size_t i) { return pass_digit(p, i); }, p.hist + (size_t)blockIdx.x * radix);
 }
 
-__global__ void __launch_bounds__(kSortThreads) pass_scatter_kernel(Pass p) {
+__global__ void __launch_bounds__(kSortThreads) pass_scatter_kernel(Pass p, ZeroJob zero) {
+  if (blockIdx.x >= p.tiles) {
+    zero_piece(zero, zero.done + blockIdx.x - p.tiles);
+    return;
+  }
   __shared__ uint32_t counts[kSortWaves * kMaxRadix];
   __shared__ uint32_t scan[kSortWaves];
   const uint32_t radix = 1u << p.bits;
   const size_t lo = (size_t)blockIdx.x * p.tile;
   const size_t hi = lo + p.tile < p.n ? lo + p.tile : p.n;
+  auto digit = [&](size_t i) { return pass_digit(p, i); };
+  const Run run = load_run(lo, hi, p.tile, digit);
   uint32_t before, total, all;
   tile_sums(p.hist, radix, p.tiles, blockIdx.x, threadIdx.x, &before, &total);
   const uint32_t first = block_scan(total, scan, &all);
-  place_items(counts, radix, p.bits, lo, hi, p.tile, first + before, [&](size_t i) { return pass_digit(p, i); },
+  place_items(counts, radix, p.bits, run, first + before, digit,
               [&](size_t i, uint32_t d, uint32_t place) {
                 if (d != kNoKey && place < p.n) {
                   p.keys_out[place] = p.keys ? p.keys[i] : load_key(p.src, i);
@@ -160,11 +216,24 @@ size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
   return n <= kRankMax ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
 }
 
-hipError_t launch_sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws,
-                           hipStream_t stream) {
+namespace {
+
+// Pieces that a launch of the sort zeroes beside it.
+constexpr uint64_t kPiecesBeside = 768;
+
+hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws, ZeroJob* zero,
+                    hipStream_t stream) {
   if (n == 0) return hipSuccess;
+  uint32_t beside = 0;
+  auto next = [&]() {
+    zero->done += beside;
+    beside = (uint32_t)(zero->pieces - zero->done < kPiecesBeside ? zero->pieces - zero->done : kPiecesBeside);
+  };
   if (n <= kRankMax) {
-    rank_kernel<<<(uint32_t)((n + 63) / 64), kSortThreads, 0, stream>>>(src, (uint32_t)n, keys, pos);
+    const uint32_t groups = (uint32_t)((n + 63) / 64);
+    next();
+    rank_kernel<<<groups + beside, kSortThreads, 0, stream>>>(src, (uint32_t)n, keys, pos, groups, *zero);
+    zero->done += beside;
     return hipGetLastError();
   }
   uint32_t bits = 1;
@@ -180,21 +249,26 @@ hipError_t launch_sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint3
     p.bits = per;
     p.keys_out = last_buffer ? keys : tmp_keys;
     p.pos_out = last_buffer ? pos : tmp_pos;
-    pass_histogram_kernel<<<p.tiles, kSortThreads, 0, stream>>>(p);
+    next();
+    pass_histogram_kernel<<<p.tiles + beside, kSortThreads, 0, stream>>>(p, *zero);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    pass_scatter_kernel<<<p.tiles, kSortThreads, 0, stream>>>(p);
+    next();
+    pass_scatter_kernel<<<p.tiles + beside, kSortThreads, 0, stream>>>(p, *zero);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     p.keys = p.keys_out;
     p.pos = p.pos_out;
   }
+  zero->done += beside;
   return hipSuccess;
 }
+
+}  // namespace
 
 // ---------------------------------------------------------------- the gradient
 
 namespace {
 
-constexpr uint32_t kZeroRows = 16;      // table rows per zeroing wave
+constexpr size_t kZeroBytes = 32768;    // of table rows per zeroing workgroup, 4 to 64 rows
 constexpr uint32_t kJoinCols = 256;     // columns per workgroup and round of the join: 4 fp32 per lane
 
 struct Grad {
@@ -209,7 +283,10 @@ struct Grad {
   size_t wstride;
   float* partial;           // [chunk][2][pstride]: a run that began before the chunk; one that goes on after it
   uint32_t pstride;
-  uint64_t sum_units, units;
+  uint32_t join_chunks;
+  uint32_t zero_from;       // rows before it are zero already
+  uint32_t zero_rows;       // table rows per zeroing workgroup
+  uint64_t sum_units;
 };
 
 template <typename To, int N, bool ACC>
@@ -287,66 +364,117 @@ __device__ __forceinline__ void sum_chunk(const Grad& g, uint32_t c, uint32_t sl
   }
 }
 
+// The first place in the sorted list whose key is not below v: 64 places are
+// compared at a time, so three loads in turn search 2^18 tokens.
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t* keys, uint32_t n, uint32_t v) {
+  uint32_t lo = 0;
+  while (n) {
+    const uint32_t step = (n + 63) / 64, at = lane_id() * step;
+    const uint32_t below = (uint32_t)__popcll(__ballot(at < n && keys[lo + at] < v));
+    if (!below) break;
+    const uint32_t skip = (below - 1) * step + 1;     // the last place below v, and it
+    const uint32_t rest = n - skip;
+    lo += skip;
+    n = rest < step - 1 ? rest : step - 1;
+  }
+  return lo;
+}
+
+// Which of the rows [v0, v0 + count) have tokens, count <= 64.
+__device__ __forceinline__ uint64_t rows_with_tokens(const Grad& g, uint32_t v0, uint32_t count) {
+  uint64_t found = 0;
+  uint32_t p = lower_bound(g.keys, g.n, v0);
+  for (;;) {
+    const uint32_t key = p + lane_id() < g.n ? g.keys[p + lane_id()] : kNoKey;
+    const uint32_t r = key - v0;
+    uint64_t mine = key != kNoKey && r < count ? 1ull << r : 0;
+#pragma unroll
+    for (int m = 32; m; m >>= 1) mine |= __shfl_xor(mine, m);
+    found |= mine;
+    const uint32_t last = lane_read(key, 63);
+    if (last == kNoKey || last - v0 >= count - 1) return found;
+    p = lower_bound(g.keys, g.n, last + 1);           // past the run that fills the rest
+  }
+}
+
+// A workgroup zeroes those of its rows that no token has.
 template <typename To>
 __device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
-  const uint32_t lane = lane_id(), v = v0 + lane;
-  const bool ask = lane < kZeroRows && v < g.vocab;
-  uint32_t lo = 0, hi = ask ? g.n : 0;       // the first place whose key is not below v
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (g.keys[mid] < v)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const uint32_t count = g.vocab - v0 < g.zero_rows ? g.vocab - v0 : g.zero_rows;
+  const uint64_t all = count < 64 ? (1ull << count) - 1 : ~0ull;
+  uint64_t absent = all & ~rows_with_tokens(g, v0, count);
+  const uint32_t nvec = (g.dim + To::kVec - 1) / To::kVec;
+  if (nvec > 64) {
+    while (absent) {
+      const uint32_t k = (uint32_t)__builtin_ctzll(absent);
+      absent &= absent - 1;
+      typename To::raw* row = elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride);
+      for (uint32_t v = threadIdx.x; v < nvec; v += kThreads)
+        store_vec<To>(row + (size_t)v * To::kVec, vec4{0, 0, 0, 0}, g.dim - v * To::kVec);
+    }
+    return;
   }
-  uint64_t absent = __ballot(ask && (lo == g.n || g.keys[lo] != v));
-  while (absent) {
-    const uint32_t k = (uint32_t)__builtin_ctzll(absent);
-    absent &= absent - 1;
-    typename To::raw* row = elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride);
-    for (uint32_t col = lane * To::kVec; col < g.dim; col += 64 * To::kVec)
-      store_vec<To>(row + col, vec4{0, 0, 0, 0}, g.dim - col);
+  const uint32_t lg = 32 - __builtin_clz(nvec - 1 | 1) - (nvec == 1);      // 1 << lg lanes a row
+  for (uint32_t i = threadIdx.x; i < count << lg; i += kThreads) {
+    const uint32_t k = i >> lg, v = i & ((1u << lg) - 1);
+    if (v < nvec && (absent >> k & 1))
+      store_vec<To>(elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride + (size_t)v * To::kVec),
+                            vec4{0, 0, 0, 0}, g.dim - v * To::kVec);
   }
 }
 
 template <typename Ti, typename To, bool ACC>
-__global__ void __launch_bounds__(kThreads) grad_kernel(Grad g) {
-  for (uint64_t u = (uint64_t)blockIdx.x * kWaves + wave_id(); u < g.units; u += (uint64_t)gridDim.x * kWaves) {
-    if (u < g.sum_units)
-      sum_chunk<Ti, To, ACC>(g, (uint32_t)(u / g.slices), (uint32_t)(u % g.slices));
-    else if constexpr (!ACC)
-      zero_rows<To>(g, (uint32_t)(u - g.sum_units) * kZeroRows);
+__global__ void __launch_bounds__(kThreads) grad_kernel(Grad g, uint32_t sum_blocks, uint32_t zero_blocks) {
+  for (uint64_t b = blockIdx.x; b < (uint64_t)sum_blocks + zero_blocks; b += gridDim.x) {
+    if (b < sum_blocks) {
+      const uint64_t u = b * kWaves + wave_id();
+      if (u < g.sum_units) sum_chunk<Ti, To, ACC>(g, (uint32_t)(u / g.slices), (uint32_t)(u % g.slices));
+    } else if constexpr (!ACC) {
+      zero_rows<To>(g, g.zero_from + (uint32_t)(b - sum_blocks) * g.zero_rows);
+    }
   }
 }
 
 // Adds the partials of the runs that cross chunk edges.  The chunk in which
-// such a run begins owns it; its 4 waves take every fourth of the chunks that
-// follow, and wave 0 adds the four sums in order.
+// such a run begins owns it.  A workgroup looks at join_chunks (<= 8) chunks at
+// once, one per lane, since most own none in a large batch; for one that does,
+// its 4 waves take every fourth of the chunks that follow, and wave 0 adds the
+// four sums in order.
+
 template <typename To, bool ACC>
-__global__ void __launch_bounds__(kThreads) join_kernel(Grad g) {
+__device__ __forceinline__ void join_runs(const Grad& g, uint32_t group, uint32_t col_block, uint32_t col_blocks) {
   __shared__ float lds[kWaves][kJoinCols];
   const uint32_t lane = lane_id(), w = wave_id();
-  for (uint32_t c = blockIdx.x; c + 1 < g.nchunks; c += gridDim.x) {
-    const uint32_t p0 = c * g.chunk, p1 = p0 + g.chunk;
-    const uint32_t key = g.keys[p1 - 1];
-    if (key == kNoKey || g.keys[p1] != key) continue;
-    if (p0 && g.keys[p0] == key && g.keys[p0 - 1] == key) continue;   // it began before this chunk
+  const uint32_t mine = group * g.join_chunks + lane;
+  uint32_t key = kNoKey;
+  bool owner = false;
+  if (lane < g.join_chunks && mine + 1 < g.nchunks) {
+    const uint32_t p0 = mine * g.chunk, p1 = p0 + g.chunk;
+    key = g.keys[p1 - 1];
+    owner = key != kNoKey && g.keys[p1] == key && !(p0 && g.keys[p0] == key && g.keys[p0 - 1] == key);
+  }
+  uint64_t owners = __ballot(owner);
+  while (owners) {
+    const uint32_t at = (uint32_t)__builtin_ctzll(owners);
+    owners &= owners - 1;
+    const uint32_t c = group * g.join_chunks + at, row = lane_read(key, at);
     uint32_t more = 0;     // chunks after c that begin inside the run
     for (;;) {
       const uint32_t k = c + 1 + more + lane;
-      const uint64_t same = __ballot(k < g.nchunks && g.keys[(size_t)k * g.chunk] == key);
+      const uint64_t same = __ballot(k < g.nchunks && g.keys[(size_t)k * g.chunk] == row);
       const uint32_t run = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
       more += run;
       if (run < 64) break;
     }
-    for (uint32_t col = blockIdx.y * kJoinCols + lane * 4; col - lane * 4 < g.dim; col += gridDim.y * kJoinCols) {
+    for (uint32_t c0 = col_block * kJoinCols; c0 < g.dim; c0 += col_blocks * kJoinCols) {
+      const uint32_t col = c0 + lane * 4;
       float acc[4] = {0, 0, 0, 0};
       if (col < g.dim) {
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t i = w; i < more; i += kWaves) {
-          const float* p = g.partial + (size_t)(c + 1 + i) * 2 * g.pstride + col;
+          const vec4 p = *reinterpret_cast<const vec4*>(g.partial + (size_t)(c + 1 + i) * 2 * g.pstride + col);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] += p[j];
+          for (int j = 0; j < 4; ++j) acc[j] += bits_f32(p[j]);
         }
       }
 #pragma unroll
@@ -360,11 +488,24 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Grad g) {
           sum[j] = p[j];
           for (int k = 0; k < kWaves; ++k) sum[j] += lds[k][lane * 4 + j];
         }
-        write_row<To, 4, ACC>(g, key, col, sum);
+        write_row<To, 4, ACC>(g, row, col, sum);
       }
       __syncthreads();
     }
   }
+}
+
+// The joins, and the last of the zeroing beside them.
+template <typename To, bool ACC>
+__global__ void __launch_bounds__(kThreads) join_kernel(Grad g, uint32_t join_blocks, uint32_t col_blocks,
+                                                        uint32_t zero_done) {
+  if (blockIdx.x < join_blocks) {
+    const uint32_t groups = (g.nchunks - 1 + g.join_chunks - 1) / g.join_chunks;
+    for (uint32_t i = blockIdx.x / col_blocks; i < groups; i += join_blocks / col_blocks)
+      join_runs<To, ACC>(g, i, blockIdx.x % col_blocks, col_blocks);
+    return;
+  }
+  if constexpr (!ACC) zero_rows<To>(g, g.zero_from + (zero_done + blockIdx.x - join_blocks) * g.zero_rows);
 }
 
 // Tokens per chunk (<= 64): as many as leave some 4096 waves to the sums.
@@ -391,17 +532,29 @@ GradLayout grad_layout(size_t n, size_t vocab, size_t dim) {
 }
 
 template <typename Ti, typename To, bool ACC>
-hipError_t run_grad(const Grad& g, hipStream_t stream) {
-  if (g.units) {
-    grad_kernel<Ti, To, ACC><<<blocks_for(g.units), kThreads, 0, stream>>>(g);
+hipError_t run_grad(Grad g, hipStream_t stream) {
+  // A share of the zeroing runs beside the joins, which by themselves are a
+  // few workgroups waiting for memory.
+  const bool joins = g.nchunks > 1;
+  const uint32_t zero_blocks = (uint32_t)(((uint64_t)g.vocab - g.zero_from + g.zero_rows - 1) / g.zero_rows);
+  uint32_t later = joins ? zero_blocks / 4 : 0;
+  if (later > kMaxBlocks) later = kMaxBlocks;
+  const uint32_t now = zero_blocks - later, sum_blocks = (uint32_t)((g.sum_units + kWaves - 1) / kWaves);
+  const uint64_t blocks = (uint64_t)sum_blocks + now;
+  if (blocks) {
+    grad_kernel<Ti, To, ACC><<<(uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks), kThreads, 0, stream>>>(
+        g, sum_blocks, now);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (g.nchunks > 1) {
-    const uint32_t cols = (g.dim + kJoinCols - 1) / kJoinCols;
-    join_kernel<To, ACC><<<dim3(g.nchunks - 1 < 65536 ? g.nchunks - 1 : 65536, cols < 8 ? cols : 8), kThreads, 0, stream>>>(g);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  if (!joins) return hipSuccess;
+  const uint32_t cols = (g.dim + kJoinCols - 1) / kJoinCols, col_blocks = cols < 8 ? cols : 8;
+  // enough chunks per workgroup for one round of workgroups, some 2048
+  const uint64_t all = (uint64_t)g.nchunks * col_blocks;
+  g.join_chunks = all >= 2048 * 8 ? 8 : all <= 2048 ? 1 : (uint32_t)(all / 2048);
+  const uint32_t groups = (g.nchunks - 1 + g.join_chunks - 1) / g.join_chunks;
+  const uint32_t join_blocks = (groups < 65536 ? groups : 65536) * col_blocks;
+  join_kernel<To, ACC><<<join_blocks + later, kThreads, 0, stream>>>(g, join_blocks, col_blocks, now);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -414,13 +567,15 @@ hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* we
   while (lg < 6 && (1u << lg) < nvec) ++lg;
   const uint32_t slices = (nvec + 64 * U - 1) / (64 * U);
   const uint64_t units = (uint64_t)((ntokens + (64u >> lg) - 1) / (64u >> lg)) * slices;
-  if (dtype == HC_F32)
-    embedding_kernel<F32, U><<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride,
-                                                                         scale, out, ostride, lg, slices, units);
-  else
-    embedding_kernel<BF16, U><<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride,
-                                                                          scale, out, ostride, lg, slices, units);
-  return hipGetLastError();
+  const uint32_t blocks = blocks_for(units);
+  auto launch = [&](auto kernel) {
+    kernel<<<blocks, kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride, scale, out, ostride, lg,
+                                            slices, units);
+    return hipGetLastError();
+  };
+  const bool nt = ntokens * dim * (dtype == HC_F32 ? 4 : 2) >= kStreamStoreBytes;
+  if (dtype == HC_F32) return nt ? launch(embedding_kernel<F32, U, true>) : launch(embedding_kernel<F32, U, false>);
+  return nt ? launch(embedding_kernel<BF16, U, true>) : launch(embedding_kernel<BF16, U, false>);
 }
 
 size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) { return grad_layout(ntokens, vocab, dim).bytes; }
@@ -432,7 +587,19 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   char* base = static_cast<char*>(ws);
   uint32_t* keys = reinterpret_cast<uint32_t*>(base + l.keys);
   uint32_t* pos = reinterpret_cast<uint32_t*>(base + l.pos);
-  if (hipError_t e = launch_sort_ids(src, ntokens, keys, pos, base + l.sort, stream); e != hipSuccess) return e;
+  const size_t row_bytes = dim * (dwtype == HC_F32 ? 4 : 2), stride = wstride * (dwtype == HC_F32 ? 4 : 2);
+  ZeroJob zero;
+  if (!accumulate) {
+    zero.base = static_cast<char*>(dweight);
+    zero.flat = stride == row_bytes || src.nkeys == 1;
+    zero.rows = zero.flat ? 1 : src.nkeys;
+    zero.row_bytes = zero.flat ? row_bytes * src.nkeys : row_bytes;
+    zero.stride = stride;
+    zero.rows_per_piece = row_bytes < kPieceBytes ? kPieceBytes / row_bytes : 1;
+    zero.pieces = zero.flat ? (zero.row_bytes + kPieceBytes - 1) / kPieceBytes
+                            : (zero.rows + zero.rows_per_piece - 1) / zero.rows_per_piece;
+  }
+  if (hipError_t e = sort_ids(src, ntokens, keys, pos, base + l.sort, &zero, stream); e != hipSuccess) return e;
   Grad g = {};
   g.keys = keys;
   g.pos = pos;
@@ -451,7 +618,11 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   g.partial = reinterpret_cast<float*>(base + l.partial);
   g.pstride = (g.dim + 3) / 4 * 4;
   g.sum_units = (uint64_t)g.nchunks * g.slices;
-  g.units = g.sum_units + (accumulate ? 0 : (g.vocab + kZeroRows - 1) / kZeroRows);
+  const uint64_t zeroed = zero.done == zero.pieces ? src.nkeys
+                          : zero.flat              ? zero.done * kPieceBytes / row_bytes
+                                                   : zero.done * zero.rows_per_piece;
+  g.zero_from = accumulate ? g.vocab : (uint32_t)zeroed;
+  g.zero_rows = row_bytes >= kZeroBytes / 4 ? 4 : row_bytes <= kZeroBytes / 64 ? 64 : (uint32_t)(kZeroBytes / row_bytes);
   if (dtype == HC_F32) {
     if (dwtype == HC_F32)
       return accumulate ? run_grad<F32, F32, true>(g, stream) : run_grad<F32, F32, false>(g, stream);

@@ -26,7 +26,7 @@ constexpr uint32_t kChunkBytes = 16384;
 constexpr uint32_t kVecs = kChunkBytes / 16 / kThreads;   // 16-byte vectors per lane and chunk
 constexpr uint32_t kBatch = 128;        // tensors per kernel argument: 3.6 KB of the 4 KB
 constexpr uint32_t kMaxGrid = 2048;     // 8 workgroups of 4 waves on each of 256 CUs
-constexpr uint32_t kStreamChunks = (320u << 20) / kChunkBytes;
+constexpr uint32_t kStreamChunks = (uint32_t)(kStreamStoreBytes / kChunkBytes);
 constexpr uint32_t kFuseChunks = (128u << 20) / kChunkBytes;
 constexpr uint64_t kBf16Bit = 1ull << 63;
 

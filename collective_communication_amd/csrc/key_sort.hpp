@@ -23,9 +23,10 @@ constexpr uint32_t kMaxRadix = 1024;
 constexpr uint32_t kMaxTiles = 64;
 constexpr uint32_t kMinTile = 1024;     // items
 
-// Items per tile, a multiple of 1024 (64 per wave), for at most kMaxTiles tiles.
+// Items per tile, a multiple of 1024 (64 per wave), for at most kMaxTiles
+// tiles; up to 4096 items are one tile, which needs no histogram launch.
 inline uint32_t sort_tile(size_t n) {
-  const size_t per = (n + kMaxTiles - 1) / kMaxTiles;
+  const size_t per = n <= 4 * kMinTile ? n : (n + kMaxTiles - 1) / kMaxTiles;
   const size_t t = (per + kMinTile - 1) / kMinTile * kMinTile;
   return (uint32_t)(t < kMinTile ? kMinTile : t);
 }
@@ -85,36 +86,64 @@ __device__ __forceinline__ void tile_histogram(uint32_t* lds, uint32_t radix, si
 }
 
 // Per digit: the sum of the tiles' counts before `tile`, and over all tiles.
+// All loads of 32 tiles are in flight at once.
 __device__ __forceinline__ void tile_sums(const uint32_t* hist, uint32_t radix, uint32_t tiles, uint32_t tile,
                                           uint32_t d, uint32_t* before, uint32_t* total) {
   uint32_t b = 0, a = 0;
   if (d < radix) {
-#pragma unroll 8
-    for (uint32_t t = 0; t < tiles; ++t) {
-      const uint32_t c = hist[(size_t)t * radix + d];
-      b += t < tile ? c : 0;
-      a += c;
+    for (uint32_t t0 = 0; t0 < tiles; t0 += 32) {
+      uint32_t c[32];
+#pragma unroll
+      for (uint32_t i = 0; i < 32; ++i) c[i] = t0 + i < tiles ? hist[(size_t)(t0 + i) * radix + d] : 0;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (uint32_t i = 0; i < 32; ++i) {
+        b += t0 + i < tile ? c[i] : 0;
+        a += c[i];
+      }
     }
   }
   *before = b;
   *total = a;
 }
 
-// Hands each item of [lo, hi) its place: put(i, digit, place) with place =
-// base(its digit) + how many items of the tile before it have the same digit.
-// counts: kSortWaves x radix words of LDS; base(d): the digit's first place
-// for this tile, called once by thread d.  Items without a key: put(i, kNoKey, 0).
+// A wave's items of its tile: a contiguous run, 64 at a time.  The first
+// kHeld rounds' digits stay in registers, which is all of them in tiles of up
+// to 4096 items; later ones are read again when they are placed.
+constexpr uint32_t kHeld = 4;
+struct Run {
+  size_t begin, end;
+  uint32_t held[kHeld];
+};
+template <typename Digit>
+__device__ __forceinline__ Run load_run(size_t lo, size_t hi, uint32_t tile_items, Digit digit) {
+  Run r;
+  const uint32_t run = tile_items / kSortWaves;
+  r.begin = lo + (size_t)wave_id() * run;
+  r.end = r.begin + run < hi ? r.begin + run : hi;
+#pragma unroll
+  for (uint32_t k = 0; k < kHeld; ++k) {
+    const size_t i = r.begin + k * 64 + lane_id();
+    r.held[k] = i < r.end ? digit(i) : kNoKey;
+  }
+  return r;
+}
+
+// Hands each item of the run its place: put(i, digit, place) with place = the
+// digit's first place for this tile (my_base, of digit threadIdx.x) + how many
+// items of the tile before it have the same digit.  counts: kSortWaves x radix
+// words of LDS.  Items without a key: put(i, kNoKey, 0).
 template <typename Digit, typename Put>
-__device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, uint32_t bits, size_t lo, size_t hi,
-                                            uint32_t tile_items, uint32_t my_base, Digit digit, Put put) {
-  const uint32_t w = wave_id(), lane = lane_id();
-  uint32_t* mine = counts + (size_t)w * radix;
+__device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, uint32_t bits, const Run& r,
+                                            uint32_t my_base, Digit digit, Put put) {
+  const uint32_t lane = lane_id();
+  uint32_t* mine = counts + (size_t)wave_id() * radix;
   for (uint32_t d = threadIdx.x; d < radix * kSortWaves; d += kSortThreads) counts[d] = 0;
   __syncthreads();
-  const uint32_t run = tile_items / kSortWaves;
-  const size_t a = lo + (size_t)w * run;
-  const size_t b = a + run < hi ? a + run : hi;
-  for (size_t i = a + lane; i < b; i += 64) {
+#pragma unroll
+  for (uint32_t k = 0; k < kHeld; ++k)
+    if (r.held[k] != kNoKey) atomicAdd(&mine[r.held[k]], 1u);
+  for (size_t i = r.begin + kHeld * 64 + lane; i < r.end; i += 64) {
     const uint32_t d = digit(i);
     if (d != kNoKey) atomicAdd(&mine[d], 1u);
   }
@@ -129,10 +158,7 @@ __device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, ui
     }
   }
   __syncthreads();
-  for (size_t i0 = a; i0 < b; i0 += 64) {
-    const size_t i = i0 + lane;
-    const bool in = i < b;
-    const uint32_t d = in ? digit(i) : kNoKey;
+  auto place64 = [&](size_t i, uint32_t d) {
     const bool valid = d != kNoKey;
     const uint64_t same = same_digit(d, valid, bits);
     uint32_t place = 0;
@@ -143,8 +169,13 @@ __device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, ui
     if (valid && (same >> lane) == 1) mine[d] = place + 1;   // the digit's last lane
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (in) put(i, d, place);
-  }
+    if (i < r.end) put(i, d, place);
+  };
+#pragma unroll
+  for (uint32_t k = 0; k < kHeld; ++k)
+    if (r.begin + k * 64 < r.end) place64(r.begin + k * 64 + lane, r.held[k]);
+  for (size_t i0 = r.begin + kHeld * 64; i0 < r.end; i0 += 64)
+    place64(i0 + lane, i0 + lane < r.end ? digit(i0 + lane) : kNoKey);
 }
 
 }  // namespace hc

@@ -23,7 +23,7 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const s
                             const hc_dtype_t* dtypes, size_t ntensors, float max_norm, const float* d_norm, void* ws,
                             hipStream_t stream);
 
-// ---- keys (key_sort.hip)
+// ---- keys (key_sort.hpp)
 // Small integer keys made from 32- or 64-bit ids: id - start where that lies
 // in [0, nkeys) and the id is not `skip`; any other id has no key.
 struct KeySource {
@@ -35,11 +35,6 @@ struct KeySource {
   int use_skip;
 };
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;
-// Sorts n ids by key, stable: keys[] ascending, then kNoKey for the ids
-// without one; pos[] the ids' places in the input.
-size_t sort_ids_ws_bytes(size_t n, size_t nkeys);
-hipError_t launch_sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws,
-                           hipStream_t stream);
 
 // ---- embedding (embed_kernels.hip)
 hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* weight, hc_dtype_t dtype, size_t dim,
