@@ -41,13 +41,13 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
     const uint32_t v0 = (uint32_t)(u % slices) * (64 * U) + at;
     if (t >= ntokens) continue;
     const uint32_t key = load_key(src, t);
-    vec4 x[U];
+    typename T::vec x[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t v = v0 + 64 * i;
-      x[i] = vec4{0, 0, 0, 0};
+      x[i] = zero_vec<T>();
       if (key != kNoKey && v < nvec)
-        x[i] = load_vec<T>(elem<T>(weight, (size_t)key * wstride + (size_t)v * T::kVec), dim - v * T::kVec);
+        x[i] = load_vec<T>(elem<T>(weight, (size_t)key * wstride + vec_at<T>(v * T::kVec, dim)));
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
       T::unpack(x[i], f);
 #pragma unroll
       for (int j = 0; j < T::kVec; ++j) f[j] *= scale;
-      store_vec<T, NT>(elem<T>(out, t * ostride + (size_t)v * T::kVec), key == kNoKey ? vec4{0, 0, 0, 0} : T::pack(f),
-                   dim - v * T::kVec);
+      store_vec<T, NT>(elem<T>(out, t * ostride + vec_at<T>(v * T::kVec, dim)),
+                       key == kNoKey ? zero_vec<T>() : T::pack(f));
     }
   }
 }
@@ -79,12 +79,6 @@ struct ZeroJob {
   uint64_t pieces = 0, done = 0;
   bool flat = false;
 };
-
-__device__ __forceinline__ void zero_span(char* p, uint64_t bytes, uint32_t lane, uint32_t lanes) {
-  for (uint64_t i = lane * 16; i < bytes; i += lanes * 16)
-    store_vec<BF16>(reinterpret_cast<uint16_t*>(p + i), vec4{0, 0, 0, 0},
-                    bytes - i < 16 ? (uint32_t)(bytes - i) / 2 : BF16::kVec);
-}
 
 __device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
   if (z.flat) {
@@ -289,20 +283,22 @@ struct Grad {
   uint64_t sum_units;
 };
 
+// Writes N columns of a table row from `at` on; the first `skip` of them
+// belong to another lane, which has the same sums for them: written all the
+// same, unless the table's own values are added.
 template <typename To, int N, bool ACC>
-__device__ __forceinline__ void write_row(const Grad& g, uint32_t row, uint32_t col, const float* sum) {
-  typename To::raw* p = elem<To>(g.dweight, (size_t)row * g.wstride + col);
-  const uint32_t left = g.dim - col;
+__device__ __forceinline__ void write_row(const Grad& g, uint32_t row, uint32_t at, uint32_t skip, const float* sum) {
+  typename To::raw* p = elem<To>(g.dweight, (size_t)row * g.wstride + at);
   float f[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = sum[i] * g.scale;
   if constexpr (ACC) {
-    float old[N];
-    load_vals<To, N>(p, old, left);
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] += old[i];
+    for (int i = 0; i < N; ++i)
+      if ((uint32_t)i >= skip) p[i] = To::narrow(To::widen(p[i]) + f[i]);
+  } else {
+    store_vals<To, N>(p, f);
   }
-  store_vals<To, N>(p, f, left);
 }
 
 template <typename Ti, typename To, bool ACC>
@@ -322,21 +318,20 @@ __device__ __forceinline__ void sum_chunk(const Grad& g, uint32_t c, uint32_t sl
   const uint64_t ends = __ballot(lane < live && (key != after || lane == live - 1));
   const bool head = first_lane_read(key) == first_lane_read(prev);
   const bool tail = lane_read(key, live - 1) == lane_read(after, live - 1);
-  const uint32_t col = slice * 64 * N + lane * N;
+  const uint32_t col = slice * 64 * N + lane * N, at = vec_at<Ti>(col, g.dim);
   const bool mine = col < g.dim;
-  const uint32_t left = mine ? g.dim - col : 0;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.0f;
   bool first_run = true;
   for (uint32_t i = 0; i < live; i += U) {
-    vec4 x[U];
+    typename Ti::vec x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      x[u] = vec4{0, 0, 0, 0};
+      x[u] = zero_vec<Ti>();
       if (i + u < live) {
         const uint32_t row = lane_read(pos, i + u);
-        if (mine) x[u] = load_vec<Ti>(elem<Ti>(g.dout, (size_t)row * g.dstride + col), left);
+        if (mine) x[u] = load_vec<Ti>(elem<Ti>(g.dout, (size_t)row * g.dstride + at));
       }
     }
 #pragma unroll
@@ -353,10 +348,9 @@ __device__ __forceinline__ void sum_chunk(const Grad& g, uint32_t c, uint32_t sl
       const uint32_t table_row = lane_read(key, i + u);
       if (mine) {
         if (from_before || goes_on)
-          store_vals<F32, N>(elem<F32>(g.partial, ((size_t)c * 2 + (from_before ? 0 : 1)) * g.pstride + col), acc,
-                             left);
+          store_vals<F32, N>(elem<F32>(g.partial, ((size_t)c * 2 + (from_before ? 0 : 1)) * g.pstride + at), acc);
         else
-          write_row<To, N, ACC>(g, table_row, col, acc);
+          write_row<To, N, ACC>(g, table_row, at, col - at, acc);
       }
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] = 0.0f;
@@ -397,30 +391,26 @@ __device__ __forceinline__ uint64_t rows_with_tokens(const Grad& g, uint32_t v0,
   }
 }
 
-// A workgroup zeroes those of its rows that no token has.
+// A workgroup zeroes those of its rows that no token has: a row at a time, or
+// several where a row is less than a wave's vectors.
 template <typename To>
 __device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
   const uint32_t count = g.vocab - v0 < g.zero_rows ? g.vocab - v0 : g.zero_rows;
   const uint64_t all = count < 64 ? (1ull << count) - 1 : ~0ull;
   uint64_t absent = all & ~rows_with_tokens(g, v0, count);
-  const uint32_t nvec = (g.dim + To::kVec - 1) / To::kVec;
+  const uint64_t bytes = (uint64_t)g.dim * sizeof(typename To::raw), nvec = (bytes + 15) / 16;
+  auto row = [&](uint32_t k) { return reinterpret_cast<char*>(elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride)); };
   if (nvec > 64) {
     while (absent) {
       const uint32_t k = (uint32_t)__builtin_ctzll(absent);
       absent &= absent - 1;
-      typename To::raw* row = elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride);
-      for (uint32_t v = threadIdx.x; v < nvec; v += kThreads)
-        store_vec<To>(row + (size_t)v * To::kVec, vec4{0, 0, 0, 0}, g.dim - v * To::kVec);
+      zero_span(row(k), bytes, threadIdx.x, kThreads);
     }
     return;
   }
-  const uint32_t lg = 32 - __builtin_clz(nvec - 1 | 1) - (nvec == 1);      // 1 << lg lanes a row
-  for (uint32_t i = threadIdx.x; i < count << lg; i += kThreads) {
-    const uint32_t k = i >> lg, v = i & ((1u << lg) - 1);
-    if (v < nvec && (absent >> k & 1))
-      store_vec<To>(elem<To>(g.dweight, (size_t)(v0 + k) * g.wstride + (size_t)v * To::kVec),
-                            vec4{0, 0, 0, 0}, g.dim - v * To::kVec);
-  }
+  const uint32_t lanes = nvec == 1 ? 8 : 1u << (32 - __builtin_clz((uint32_t)nvec - 1));   // of a row
+  for (uint32_t k = threadIdx.x / lanes; k < count; k += kThreads / lanes)
+    if (absent >> k & 1) zero_span(row(k), bytes, threadIdx.x % lanes, lanes);
 }
 
 template <typename Ti, typename To, bool ACC>
@@ -488,7 +478,13 @@ __device__ __forceinline__ void join_runs(const Grad& g, uint32_t group, uint32_
           sum[j] = p[j];
           for (int k = 0; k < kWaves; ++k) sum[j] += lds[k][lane * 4 + j];
         }
-        write_row<To, 4, ACC>(g, row, col, sum);
+        if (col + 4 <= g.dim) {
+          write_row<To, 4, ACC>(g, row, col, 0, sum);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < g.dim) write_row<To, 1, ACC>(g, row, col + j, 0, sum + j);
+        }
       }
       __syncthreads();
     }
@@ -536,6 +532,8 @@ hipError_t run_grad(Grad g, hipStream_t stream) {
   // A share of the zeroing runs beside the joins, which by themselves are a
   // few workgroups waiting for memory.
   const bool joins = g.nchunks > 1;
+  g.slices = (g.dim + 64 * Ti::kVec - 1) / (64 * Ti::kVec);
+  g.sum_units = (uint64_t)g.nchunks * g.slices;
   const uint32_t zero_blocks = (uint32_t)(((uint64_t)g.vocab - g.zero_from + g.zero_rows - 1) / g.zero_rows);
   uint32_t later = joins ? zero_blocks / 4 : 0;
   if (later > kMaxBlocks) later = kMaxBlocks;
@@ -561,21 +559,24 @@ hipError_t run_grad(Grad g, hipStream_t stream) {
 
 hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* weight, hc_dtype_t dtype, size_t dim,
                             size_t wstride, float scale, void* out, size_t ostride, hipStream_t stream) {
-  constexpr int U = 2;
-  const uint32_t nvec = (uint32_t)((dim + (dtype == HC_F32 ? 3 : 7)) / (dtype == HC_F32 ? 4 : 8));
-  uint32_t lg = 0;
-  while (lg < 6 && (1u << lg) < nvec) ++lg;
-  const uint32_t slices = (nvec + 64 * U - 1) / (64 * U);
-  const uint64_t units = (uint64_t)((ntokens + (64u >> lg) - 1) / (64u >> lg)) * slices;
-  const uint32_t blocks = blocks_for(units);
-  auto launch = [&](auto kernel) {
-    kernel<<<blocks, kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride, scale, out, ostride, lg,
-                                            slices, units);
-    return hipGetLastError();
+  auto run = [&](auto type) {
+    typedef decltype(type) T;
+    constexpr int U = 2;
+    const uint32_t nvec = (uint32_t)((dim + T::kVec - 1) / T::kVec);
+    uint32_t lg = 0;
+    while (lg < 6 && (1u << lg) < nvec) ++lg;
+    const uint32_t slices = (nvec + 64 * U - 1) / (64 * U);
+    const uint64_t units = (uint64_t)((ntokens + (64u >> lg) - 1) / (64u >> lg)) * slices;
+    auto launch = [&](auto kernel) {
+      kernel<<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride, scale, out,
+                                                         ostride, lg, slices, units);
+      return hipGetLastError();
+    };
+    return ntokens * dim * sizeof(typename T::raw) >= kStreamStoreBytes ? launch(embedding_kernel<T, U, true>)
+                                                                        : launch(embedding_kernel<T, U, false>);
   };
-  const bool nt = ntokens * dim * (dtype == HC_F32 ? 4 : 2) >= kStreamStoreBytes;
-  if (dtype == HC_F32) return nt ? launch(embedding_kernel<F32, U, true>) : launch(embedding_kernel<F32, U, false>);
-  return nt ? launch(embedding_kernel<BF16, U, true>) : launch(embedding_kernel<BF16, U, false>);
+  if (dtype == HC_F32) return dim < F32::kVec ? run(F32S{}) : run(F32{});
+  return dim < BF16::kVec ? run(BF16S{}) : run(BF16{});
 }
 
 size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) { return grad_layout(ntokens, vocab, dim).bytes; }
@@ -607,8 +608,6 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   g.chunk = chunk_tokens(ntokens, dim);
   g.nchunks = (g.n + g.chunk - 1) / g.chunk;
   g.dim = (uint32_t)dim;
-  const uint32_t width = 64 * (dtype == HC_F32 ? 4 : 8);
-  g.slices = (g.dim + width - 1) / width;
   g.vocab = src.nkeys;
   g.dout = dout;
   g.dstride = dstride;
@@ -617,20 +616,19 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   g.wstride = wstride;
   g.partial = reinterpret_cast<float*>(base + l.partial);
   g.pstride = (g.dim + 3) / 4 * 4;
-  g.sum_units = (uint64_t)g.nchunks * g.slices;
   const uint64_t zeroed = zero.done == zero.pieces ? src.nkeys
                           : zero.flat              ? zero.done * kPieceBytes / row_bytes
                                                    : zero.done * zero.rows_per_piece;
   g.zero_from = accumulate ? g.vocab : (uint32_t)zeroed;
   g.zero_rows = row_bytes >= kZeroBytes / 4 ? 4 : row_bytes <= kZeroBytes / 64 ? 64 : (uint32_t)(kZeroBytes / row_bytes);
-  if (dtype == HC_F32) {
-    if (dwtype == HC_F32)
-      return accumulate ? run_grad<F32, F32, true>(g, stream) : run_grad<F32, F32, false>(g, stream);
-    return accumulate ? run_grad<F32, BF16, true>(g, stream) : run_grad<F32, BF16, false>(g, stream);
-  }
-  if (dwtype == HC_F32)
-    return accumulate ? run_grad<BF16, F32, true>(g, stream) : run_grad<BF16, F32, false>(g, stream);
-  return accumulate ? run_grad<BF16, BF16, true>(g, stream) : run_grad<BF16, BF16, false>(g, stream);
+  auto run = [&](auto in, auto table) {
+    typedef decltype(in) Ti;
+    typedef decltype(table) To;
+    return accumulate ? run_grad<Ti, To, true>(g, stream) : run_grad<Ti, To, false>(g, stream);
+  };
+  auto run_in = [&](auto in) { return dwtype == HC_F32 ? run(in, F32{}) : run(in, BF16{}); };
+  if (dtype == HC_F32) return dim < F32::kVec ? run_in(F32S{}) : run_in(F32{});
+  return dim < BF16::kVec ? run_in(BF16S{}) : run_in(BF16{});
 }
 
 }  // namespace hc

@@ -12,6 +12,8 @@
 // other is not read k times over.  Sums run over j in order within a lane:
 // no atomics.  The token's row numbers are loaded once into the wave's lanes
 // and read from there as scalars, so every row's address is scalar.
+#include <type_traits>
+
 #include "key_sort.hpp"
 #include "launch.hpp"
 
@@ -124,7 +126,7 @@ __device__ __forceinline__ void zero_padding(const Rows& r, uint64_t unit) {
     for (uint32_t row = g; row < end && row < g + kPadRows; ++row) {
       typename T::raw* p = elem<T>(r.out, (size_t)row * r.ostride);
       for (uint32_t c = lane_id() * T::kVec; c < r.dim; c += 64 * T::kVec)
-        store_vec<T, NT>(p + c, vec4{0, 0, 0, 0}, r.dim - c);
+        store_vec<T, NT>(p + vec_at<T>(c, r.dim), zero_vec<T>());
     }
   }
 }
@@ -143,11 +145,11 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
     const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
     uint64_t there = __ballot(row >= 0);
     if (!there) continue;
-    vec4 v[U];
+    typename T::vec v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t c = c0 + i * 64 * T::kVec;
-      if (c < r.dim) v[i] = load_vec<T>(elem<T>(r.x, t * r.xstride + c), r.dim - c);
+      if (c < r.dim) v[i] = load_vec<T>(elem<T>(r.x, t * r.xstride + vec_at<T>(c, r.dim)));
     }
     while (there) {
       const uint32_t j = (uint32_t)__builtin_ctzll(there);
@@ -156,14 +158,14 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const uint32_t c = c0 + i * 64 * T::kVec;
-        if (c < r.dim) store_vec<T, NT>(elem<T>(r.out, base + c), v[i], r.dim - c);
+        if (c < r.dim) store_vec<T, NT>(elem<T>(r.out, base + vec_at<T>(c, r.dim)), v[i]);
       }
     }
   }
 }
 
 // A wave sums a slice of 64 vectors of one token's rows, four rows in flight.
-template <typename T, bool WEIGHTED, bool NT>
+template <typename T, bool WEIGHTED, bool NTL, bool NT>
 __global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
   constexpr int N = T::kVec, J = 4;
   const uint32_t lane = lane_id();
@@ -174,22 +176,23 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
     const uint32_t w = WEIGHTED && lane < r.k ? f32_bits(r.weights[t * r.k + lane]) : f32_bits(1.0f);
     uint64_t there = __ballot(row >= 0);
     const bool mine = c < r.dim;    // every lane stays, for the lane reads below
+    const uint32_t at = vec_at<T>(c, r.dim);
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     while (there) {
-      vec4 v[J];
+      typename T::vec v[J];
       float g[J];
 #pragma unroll
       for (int q = 0; q < J; ++q) {
         g[q] = 0.0f;
-        v[q] = vec4{0, 0, 0, 0};
+        v[q] = zero_vec<T>();
         if (!there) continue;
         const uint32_t j = (uint32_t)__builtin_ctzll(there);
         there &= there - 1;
         g[q] = bits_f32(lane_read(w, j));
         const size_t base = (size_t)lane_read((uint32_t)row, j) * r.rstride;
-        if (mine) v[q] = load_vec<T>(elem<T>(r.rows, base + c), r.dim - c);
+        if (mine) v[q] = load_vec<T, NTL>(elem<T>(r.rows, base + at));
       }
 #pragma unroll
       for (int q = 0; q < J; ++q) {
@@ -199,26 +202,26 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
         for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(g[q], f[i], acc[i]);
       }
     }
-    if (mine) store_vec<T, NT>(elem<T>(r.out, t * r.ostride + c), T::pack(acc), r.dim - c);
+    if (mine) store_vec<T, NT>(elem<T>(r.out, t * r.ostride + at), T::pack(acc));
   }
 }
 
-// A workgroup takes a token, its waves sharing the token's slices; each row's
+// A workgroup of WPT waves takes a token, the waves sharing its slices; each row's
 // dot product is summed over a lane's slices, then over lanes and waves in a
 // fixed order.  J slots at a time: their rows' loads are in flight together
-// with the token's.  The rows are read once, so non-temporal.
-// Measured, 16384 tokens x 8 slots x 4096 bf16 (2.28 GB): 439 us, 5.2 TB/s,
-// what a large copy reaches; one wave per token 467, J = 2 or 8 448 and 443,
-// plain loads of the rows 447, plain stores 485.
-template <typename T, bool NT>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(Rows r) {
+// with the token's.
+// Measured, 16384 tokens x 8 slots x 4096 bf16 (2.28 GB): 426 us, 5.4 TB/s, as
+// a large copy; one wave per token 467, J = 2 or 8 448 and 443, plain loads of
+// the rows 447, plain stores 485.
+template <typename T, int WPT, bool NTL, bool NT>
+__global__ void __launch_bounds__(WPT * 64) combine_grad_kernel(Rows r) {
   constexpr int N = T::kVec, J = 4;
-  __shared__ float part[kWaves][J];
+  __shared__ float part[WPT][J];
   const uint32_t lane = lane_id(), wave = wave_id();
-  const uint64_t pad_blocks = (r.padding + kWaves - 1) / kWaves;
+  const uint64_t pad_blocks = (r.padding + WPT - 1) / WPT;
   for (uint64_t u = blockIdx.x; u < r.units; u += gridDim.x) {
     if (u < pad_blocks) {
-      if (u * kWaves + wave < r.padding) zero_padding<T, NT>(r, u * kWaves + wave);
+      if (u * WPT + wave < r.padding) zero_padding<T, NT>(r, u * WPT + wave);
       continue;
     }
     const size_t t = u - pad_blocks;
@@ -246,13 +249,14 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(Rows r) {
         g[q] = bits_f32(lane_read(w, slot[q]));
         live = q + 1;
       }
-      for (uint32_t c = threadIdx.x * N; c < r.dim; c += kThreads * N) {
-        vec4 v[J];
-        const vec4 d = load_vec<T>(elem<T>(r.x, t * r.xstride + c), r.dim - c);
+      for (uint32_t c = threadIdx.x * N; c < r.dim; c += WPT * 64 * N) {
+        typename T::vec v[J];
+        const uint32_t at = vec_at<T>(c, r.dim), skip = c - at;
+        const typename T::vec d = load_vec<T>(elem<T>(r.x, t * r.xstride + at));
 #pragma unroll
         for (int q = 0; q < J; ++q) {
-          v[q] = vec4{0, 0, 0, 0};
-          if (q < live) v[q] = load_vec<T, true>(elem<T>(r.rows, rbase[q] + c), r.dim - c);
+          v[q] = zero_vec<T>();
+          if (q < live) v[q] = load_vec<T, NTL>(elem<T>(r.rows, rbase[q] + at));
         }
         float fd[N];
         T::unpack(d, fd);
@@ -263,10 +267,12 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(Rows r) {
           T::unpack(v[q], f);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            dot[q] = __builtin_fmaf(fd[i], f[i], dot[q]);
+            // a vector moved back counts its own elements only
+            const float more = __builtin_fmaf(fd[i], f[i], dot[q]);
+            dot[q] = (uint32_t)i >= skip ? more : dot[q];
             o[i] = g[q] * fd[i];
           }
-          store_vec<T, NT>(elem<T>(r.out, obase[q] + c), T::pack(o), r.dim - c);
+          store_vec<T, NT>(elem<T>(r.out, obase[q] + at), T::pack(o));
         }
       }
 #pragma unroll
@@ -274,23 +280,34 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(Rows r) {
 #pragma unroll
         for (int m = 32; m; m >>= 1) dot[q] += __shfl_xor(dot[q], m);
       }
-      if (lane == 0) {
+      if constexpr (WPT > 1) {
+        if (lane == 0) {
 #pragma unroll
-        for (int q = 0; q < J; ++q) part[wave][q] = dot[q];
-      }
-      __syncthreads();
+          for (int q = 0; q < J; ++q) part[wave][q] = dot[q];
+        }
+        __syncthreads();
 #pragma unroll
-      for (int q = 0; q < J; ++q) {
-        const float sum = (part[0][q] + part[1][q]) + (part[2][q] + part[3][q]);
-        if (lane == slot[q]) dw = sum;
+        for (int q = 0; q < J; ++q) {
+          dot[q] = 0.0f;
+#pragma unroll
+          for (int w2 = 0; w2 < WPT; ++w2) dot[q] += part[w2][q];
+        }
+        __syncthreads();
       }
-      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < J; ++q)
+        if (lane == slot[q]) dw = dot[q];
     }
     if (wave == 0 && lane < r.k) r.dweights[t * r.k + lane] = dw;
   }
 }
 
-constexpr int kDispatchU = 2;
+// fn(T{}) for the type, by single elements where a row is less than a vector.
+template <typename Fn>
+hipError_t with_type(hc_dtype_t dtype, size_t dim, Fn fn) {
+  if (dtype == HC_F32) return dim < F32::kVec ? fn(F32S{}) : fn(F32{});
+  return dim < BF16::kVec ? fn(BF16S{}) : fn(BF16{});
+}
 
 Rows rows_of(const hc_expert_plan_t& plan, size_t dim) {
   Rows r = {};
@@ -343,67 +360,78 @@ hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan
 hipError_t launch_expert_dispatch(const void* x, hc_dtype_t dtype, size_t dim, size_t xstride,
                                   const hc_expert_plan_t& plan, void* rows, size_t rstride, hipStream_t stream) {
   Rows r = rows_of(plan, dim);
-  const uint32_t width = kDispatchU * 64 * (dtype == HC_F32 ? 4 : 8);
-  r.slices = (r.dim + width - 1) / width;
   r.x = x;
   r.xstride = xstride;
   r.out = rows;
   r.ostride = rstride;
-  r.units = r.padding + (uint64_t)r.ntokens * r.slices;
-  if (!r.units) return hipSuccess;
-  const uint32_t blocks = blocks_for(r.units);
-  // the rows in use number at most ntokens * k and the padding
-  const bool nt = plan.ntokens * (size_t)plan.k * dim * (dtype == HC_F32 ? 4 : 2) >= kStreamStoreBytes;
-  if (dtype == HC_F32) {
-    if (nt)
-      dispatch_kernel<F32, kDispatchU, true><<<blocks, kThreads, 0, stream>>>(r);
+  return with_type(dtype, dim, [&](auto type) {
+    typedef decltype(type) T;
+    constexpr int U = 2;
+    r.slices = (r.dim + U * 64 * T::kVec - 1) / (U * 64 * T::kVec);
+    r.units = r.padding + (uint64_t)r.ntokens * r.slices;
+    if (!r.units) return hipSuccess;
+    const uint32_t blocks = blocks_for(r.units);
+    // the rows in use number at most ntokens * k and the padding
+    if (r.ntokens * r.k * r.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
+      dispatch_kernel<T, U, true><<<blocks, kThreads, 0, stream>>>(r);
     else
-      dispatch_kernel<F32, kDispatchU, false><<<blocks, kThreads, 0, stream>>>(r);
-  } else {
-    if (nt)
-      dispatch_kernel<BF16, kDispatchU, true><<<blocks, kThreads, 0, stream>>>(r);
-    else
-      dispatch_kernel<BF16, kDispatchU, false><<<blocks, kThreads, 0, stream>>>(r);
-  }
-  return hipGetLastError();
-}
-
-template <typename T, bool WEIGHTED>
-static hipError_t run_combine(const Rows& r, hipStream_t stream) {
-  if (r.ntokens * r.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
-    combine_kernel<T, WEIGHTED, true><<<blocks_for(r.units), kThreads, 0, stream>>>(r);
-  else
-    combine_kernel<T, WEIGHTED, false><<<blocks_for(r.units), kThreads, 0, stream>>>(r);
-  return hipGetLastError();
+      dispatch_kernel<T, U, false><<<blocks, kThreads, 0, stream>>>(r);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_expert_combine(const void* rows, hc_dtype_t dtype, size_t dim, size_t rstride,
                                  const hc_expert_plan_t& plan, const float* weights, void* out, size_t ostride,
                                  hipStream_t stream) {
   Rows r = rows_of(plan, dim);
-  const uint32_t width = 64 * (dtype == HC_F32 ? 4 : 8);
-  r.slices = (r.dim + width - 1) / width;
   r.rows = rows;
   r.rstride = rstride;
   r.weights = weights;
   r.out = out;
   r.ostride = ostride;
-  r.units = (uint64_t)r.ntokens * r.slices;
-  if (!r.units) return hipSuccess;
-  if (dtype == HC_F32) return weights ? run_combine<F32, true>(r, stream) : run_combine<F32, false>(r, stream);
-  return weights ? run_combine<BF16, true>(r, stream) : run_combine<BF16, false>(r, stream);
+  return with_type(dtype, dim, [&](auto type) {
+    typedef decltype(type) T;
+    r.slices = (r.dim + 64 * T::kVec - 1) / (64 * T::kVec);
+    r.units = (uint64_t)r.ntokens * r.slices;
+    if (!r.units) return hipSuccess;
+    auto launch = [&](auto kernel) {
+      kernel<<<blocks_for(r.units), kThreads, 0, stream>>>(r);
+      return hipGetLastError();
+    };
+    const size_t bytes = r.ntokens * r.dim * sizeof(typename T::raw);
+    const bool nts = bytes >= kStreamStoreBytes, ntl = bytes * r.k >= kStreamLoadBytes;
+    auto pick = [&](auto weighted) {
+      constexpr bool W = decltype(weighted)::value;
+      if (ntl) return nts ? launch(combine_kernel<T, W, true, true>) : launch(combine_kernel<T, W, true, false>);
+      return nts ? launch(combine_kernel<T, W, false, true>) : launch(combine_kernel<T, W, false, false>);
+    };
+    return weights ? pick(std::true_type{}) : pick(std::false_type{});
+  });
 }
 
-template <typename T>
+template <typename T, int WPT>
 static hipError_t run_combine_grad(Rows r, hipStream_t stream) {
-  r.units = (r.padding + kWaves - 1) / kWaves + r.ntokens;
+  r.units = (r.padding + WPT - 1) / WPT + r.ntokens;
   if (!r.units) return hipSuccess;
   const uint32_t blocks = (uint32_t)(r.units < kMaxBlocks ? r.units : kMaxBlocks);
-  if (r.ntokens * r.k * r.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
-    combine_grad_kernel<T, true><<<blocks, kThreads, 0, stream>>>(r);
+  const size_t bytes = r.ntokens * r.k * r.dim * sizeof(typename T::raw);
+  static_assert(kStreamLoadBytes >= kStreamStoreBytes, "streamed rows have streamed gradients");
+  if (bytes >= kStreamLoadBytes)
+    combine_grad_kernel<T, WPT, true, true><<<blocks, WPT * 64, 0, stream>>>(r);
+  else if (bytes >= kStreamStoreBytes)
+    combine_grad_kernel<T, WPT, false, true><<<blocks, WPT * 64, 0, stream>>>(r);
   else
-    combine_grad_kernel<T, false><<<blocks, kThreads, 0, stream>>>(r);
+    combine_grad_kernel<T, WPT, false, false><<<blocks, WPT * 64, 0, stream>>>(r);
   return hipGetLastError();
+}
+template <typename T>
+static hipError_t run_combine_grad(const Rows& r, hipStream_t stream) {
+  // as many waves as a row has work for: 60000 tokens x 6 slots x 64 bf16 take
+  // 55 us by one wave a token, 192 by four
+  const uint32_t nvec = (r.dim + T::kVec - 1) / T::kVec;
+  if (nvec <= 64) return run_combine_grad<T, 1>(r, stream);
+  if (nvec <= 128) return run_combine_grad<T, 2>(r, stream);
+  return run_combine_grad<T, 4>(r, stream);
 }
 
 hipError_t launch_expert_combine_grad(const void* dout, hc_dtype_t dtype, size_t dim, size_t dstride,
@@ -419,7 +447,7 @@ hipError_t launch_expert_combine_grad(const void* dout, hc_dtype_t dtype, size_t
   r.out = drows;
   r.ostride = drstride;
   r.dweights = dweights;
-  return dtype == HC_F32 ? run_combine_grad<F32>(r, stream) : run_combine_grad<BF16>(r, stream);
+  return with_type(dtype, dim, [&](auto type) { return run_combine_grad<decltype(type)>(r, stream); });
 }
 
 }  // namespace hc

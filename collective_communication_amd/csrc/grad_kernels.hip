@@ -187,13 +187,48 @@ __device__ __forceinline__ void load_full(const Place& p, vec4* v) {
   }
 }
 
-// A chunk that its tensor's ends cut: fn(element, how many are left) per vector.
-template <typename T, typename Fn>
+// A chunk that its tensor's ends cut: fn(p, first element) for its vectors of
+// type V (T, or Single<T> for a tensor narrower than one), the last one moved
+// back to end with the chunk where that has room for it; skip: how many of its
+// elements the vector before it had already.
+template <typename V, typename Fn>
 __device__ __forceinline__ void each_vec(const Place& p, Fn fn) {
-  constexpr int64_t kSize = sizeof(typename T::raw);
+  constexpr int64_t kSize = sizeof(typename V::raw);
   const int64_t lo = p.at < 0 ? 0 : p.at / kSize;
   const int64_t end = p.at + kChunkBytes < p.bytes ? p.at + kChunkBytes : p.bytes, hi = end / kSize;
-  for (int64_t i = lo + threadIdx.x * T::kVec; i < hi; i += kThreads * T::kVec) fn((size_t)i, (uint32_t)(hi - i));
+  for (int64_t i = lo + threadIdx.x * V::kVec; i < hi; i += kThreads * V::kVec) {
+    const int64_t at = i + V::kVec <= hi ? i : hi - V::kVec;
+    fn((size_t)at, (int)(i - at));
+  }
+}
+// Whether the cut chunk has room for a vector of T.
+template <typename T>
+__device__ __forceinline__ bool wide(const Place& p) {
+  const int64_t lo = p.at < 0 ? 0 : p.at, hi = p.at + kChunkBytes < p.bytes ? p.at + kChunkBytes : p.bytes;
+  return hi - lo >= (int64_t)(T::kVec * sizeof(typename T::raw));
+}
+
+template <typename T, bool INF>
+__device__ __forceinline__ void norm_cut(const Place& p, double* acc, uint32_t& big) {
+  auto add = [&](float f) {
+    if constexpr (INF) {
+      big = max(big, f32_bits(f) & 0x7FFFFFFFu);
+    } else {
+      const double d = (double)f;
+      acc[0] = __builtin_fma(d, d, acc[0]);
+    }
+  };
+  if (wide<T>(p)) {
+    each_vec<T>(p, [&](size_t at, int skip) {
+      float f[T::kVec];
+      T::unpack(load_vec<T>(elem<T>(p.src, at)), f);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i)
+        if (i >= skip) add(f[i]);
+    });
+  } else {
+    each_vec<Single<T>>(p, [&](size_t at, int) { add(T::widen(*elem<T>(p.src, at))); });
+  }
 }
 
 template <bool INF>
@@ -221,13 +256,9 @@ __device__ void norm_body(const Entry* e, const uint32_t* first, uint32_t n, uin
         for (uint32_t u = 0; u < kVecs; ++u) add_vec<F32, INF>(v[u], acc, big);
       }
     } else if (p.bf16) {
-      each_vec<BF16>(p, [&](size_t i, uint32_t left) {
-        add_vec<BF16, INF>(load_vec<BF16>(elem<BF16>(p.src, i), left), acc, big);
-      });
+      norm_cut<BF16, INF>(p, acc, big);
     } else {
-      each_vec<F32>(p, [&](size_t i, uint32_t left) {
-        add_vec<F32, INF>(load_vec<F32>(elem<F32>(p.src, i), left), acc, big);
-      });
+      norm_cut<F32, INF>(p, acc, big);
     }
     if (!more) break;
     p = next;
@@ -277,18 +308,31 @@ __device__ __forceinline__ void scale_full(const Place& p, const vec4* v, float 
     T::unpack(v[u], f);
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) f[i] *= coef;
-    store_vec<T, NT>(reinterpret_cast<typename T::raw*>(q + u * kThreads * 16), T::pack(f), T::kVec);
+    store_vec<T, NT>(reinterpret_cast<typename T::raw*>(q + u * kThreads * 16), T::pack(f));
   }
 }
+// In place a vector must not scale what another has scaled already, so the
+// last one writes its own elements only.
 template <typename T>
 __device__ __forceinline__ void scale_cut(const Place& p, float coef) {
-  each_vec<T>(p, [&](size_t i, uint32_t left) {
-    float f[T::kVec];
-    T::unpack(load_vec<T>(elem<T>(p.src, i), left), f);
+  if (wide<T>(p)) {
+    each_vec<T>(p, [&](size_t at, int skip) {
+      if (skip) {
 #pragma unroll
-    for (int j = 0; j < T::kVec; ++j) f[j] *= coef;
-    store_vec<T>(elem<T>(p.dst, i), T::pack(f), left);
-  });
+        for (int i = 0; i < T::kVec; ++i)
+          if (i >= skip) *elem<T>(p.dst, at + i) = T::narrow(T::widen(*elem<T>(p.src, at + i)) * coef);
+        return;
+      }
+      float f[T::kVec];
+      T::unpack(load_vec<T>(elem<T>(p.src, at)), f);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) f[i] *= coef;
+      store_vec<T>(elem<T>(p.dst, at), T::pack(f));
+    });
+  } else {
+    each_vec<Single<T>>(
+        p, [&](size_t at, int) { *elem<T>(p.dst, at) = T::narrow(T::widen(*elem<T>(p.src, at)) * coef); });
+  }
 }
 
 template <bool INF, bool NT>

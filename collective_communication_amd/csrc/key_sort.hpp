@@ -23,10 +23,11 @@ constexpr uint32_t kMaxRadix = 1024;
 constexpr uint32_t kMaxTiles = 64;
 constexpr uint32_t kMinTile = 1024;     // items
 
+constexpr uint32_t kHeld = 4;
 // Items per tile, a multiple of 1024 (64 per wave), for at most kMaxTiles
 // tiles; up to 4096 items are one tile, which needs no histogram launch.
 inline uint32_t sort_tile(size_t n) {
-  const size_t per = n <= 4 * kMinTile ? n : (n + kMaxTiles - 1) / kMaxTiles;
+  const size_t per = n <= kHeld * kMinTile ? n : (n + kMaxTiles - 1) / kMaxTiles;
   const size_t t = (per + kMinTile - 1) / kMinTile * kMinTile;
   return (uint32_t)(t < kMinTile ? kMinTile : t);
 }
@@ -110,7 +111,6 @@ __device__ __forceinline__ void tile_sums(const uint32_t* hist, uint32_t radix, 
 // A wave's items of its tile: a contiguous run, 64 at a time.  The first
 // kHeld rounds' digits stay in registers, which is all of them in tiles of up
 // to 4096 items; later ones are read again when they are placed.
-constexpr uint32_t kHeld = 4;
 struct Run {
   size_t begin, end;
   uint32_t held[kHeld];

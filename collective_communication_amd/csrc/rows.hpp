@@ -4,8 +4,15 @@
 // Every access is a 16-byte vector that is only element aligned: gfx950 runs
 // in unaligned access mode, so a row that starts at an odd element (an odd
 // width, a bucket's view) takes the same wide path as an aligned one.  A
-// row's last, partial vector goes element by element.  Values are widened to
-// fp32 exactly and rounded once (nearest even) where they are stored as bf16.
+// row's last vector is moved back to end where the row ends (vec_at): the
+// elements that it shares with the vector before it are read twice, computed
+// alike and written twice with the same values, and no lane branches.  Rows
+// narrower than one vector go by single elements (the types ending in S).
+// Measured, combine of 4068 tokens x 6 slots x 1031 bf16: 11.7 us so, 18.6
+// with the last vector's elements taken one by one; 1024 x 6 x 4095, 10.9 and
+// 17.7, against 10.4 at a width of 4096.
+// Values are widened to fp32 exactly and rounded once (nearest even) where
+// they are stored as bf16.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -23,14 +30,22 @@ namespace hc {
 // 67 MB 42 / 46, 134 MB 96 / 94, 201 MB 151 / 149, 537 MB 388 / 373.
 constexpr size_t kStreamStoreBytes = (size_t)128 << 20;
 
+// And launches that read at least this many bytes of rows, each once, load
+// them non-temporal: what comes straight from its producer is mostly in the
+// 256 MB Infinity Cache below that, and from memory above.  The combine of rows
+// of 4096 bf16, plain / non-temporal, us, its input just written: 134 MB 23 /
+// 26, 268 MB 48 / 53, 393 MB 87 / 76, 1.07 GB 224 / 210; three inputs in turn
+// (nothing cached): 134 MB 32 / 28, 268 MB 61 / 54, 393 MB 88 / 77.
+constexpr size_t kStreamLoadBytes = (size_t)256 << 20;
+
 typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
 typedef vec4 vec4_u __attribute__((aligned(2)));   // element aligned
 
-// Element type tags: kVec elements fill a 16-byte vector.
+// Element type tags: kVec elements are what a lane moves at once, a T::vec.
 struct F32 {
   typedef uint32_t raw;
+  typedef vec4 vec;
   static constexpr int kVec = 4;
-  static constexpr hc_dtype_t kDtype = HC_F32;
   static __device__ __forceinline__ void unpack(vec4 v, float* f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = bits_f32(v[i]);
@@ -47,8 +62,8 @@ struct F32 {
 
 struct BF16 {
   typedef uint16_t raw;
+  typedef vec4 vec;
   static constexpr int kVec = 8;
-  static constexpr hc_dtype_t kDtype = HC_BF16;
   static __device__ __forceinline__ void unpack(vec4 v, float* f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -73,6 +88,20 @@ struct BF16 {
   static __device__ __forceinline__ raw narrow(float f) { return (raw)pair(f, 0.0f); }
 };
 
+// One element per lane.
+template <typename T>
+struct Single {
+  typedef typename T::raw raw;
+  typedef typename T::raw vec;
+  static constexpr int kVec = 1;
+  static __device__ __forceinline__ void unpack(vec v, float* f) { f[0] = T::widen(v); }
+  static __device__ __forceinline__ vec pack(const float* f) { return T::narrow(f[0]); }
+  static __device__ __forceinline__ float widen(raw x) { return T::widen(x); }
+  static __device__ __forceinline__ raw narrow(float f) { return T::narrow(f); }
+};
+typedef Single<F32> F32S;
+typedef Single<BF16> BF16S;
+
 template <typename T>
 __device__ __forceinline__ const typename T::raw* elem(const void* p, size_t i) {
   return static_cast<const typename T::raw*>(p) + i;
@@ -82,73 +111,67 @@ __device__ __forceinline__ typename T::raw* elem(void* p, size_t i) {
   return static_cast<typename T::raw*>(p) + i;
 }
 
-// The vector at element p of a row with `left` (>= 1) elements from p on;
-// elements past the row's end read as zero and are not touched.
-template <typename T, bool NT = false>
-__device__ __forceinline__ vec4 load_vec(const typename T::raw* p, uint32_t left) {
-  if (left >= T::kVec) {
-    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const vec4_u*>(p));
-    return *reinterpret_cast<const vec4_u*>(p);
-  }
-  vec4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < T::kVec; ++i)
-    if ((uint32_t)i < left) {
-      if constexpr (T::kVec == 4)
-        v[i] = p[i];
-      else
-        v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    }
-  return v;
+// Where the vector that begins at column c is read and written: there, or,
+// for the last one of a row of dim >= kVec, so that it ends with the row.
+template <typename T>
+__device__ __forceinline__ uint32_t vec_at(uint32_t c, uint32_t dim) {
+  return c + T::kVec <= dim ? c : dim - T::kVec;
 }
 
 template <typename T, bool NT = false>
-__device__ __forceinline__ void store_vec(typename T::raw* p, vec4 v, uint32_t left) {
-  if (left >= T::kVec) {
+__device__ __forceinline__ typename T::vec load_vec(const typename T::raw* p) {
+  if constexpr (T::kVec == 1) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+  } else {
+    const vec4_u* q = reinterpret_cast<const vec4_u*>(p);
+    return NT ? __builtin_nontemporal_load(q) : *q;
+  }
+}
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store_vec(typename T::raw* p, typename T::vec v) {
+  if constexpr (T::kVec == 1) {
     if constexpr (NT)
-      __builtin_nontemporal_store((vec4_u)v, reinterpret_cast<vec4_u*>(p));
+      __builtin_nontemporal_store(v, p);
     else
-      *reinterpret_cast<vec4_u*>(p) = v;
-    return;
+      *p = v;
+  } else {
+    vec4_u* q = reinterpret_cast<vec4_u*>(p);
+    if constexpr (NT)
+      __builtin_nontemporal_store((vec4_u)v, q);
+    else
+      *q = v;
   }
-#pragma unroll
-  for (int i = 0; i < T::kVec; ++i)
-    if ((uint32_t)i < left) {
-      if constexpr (T::kVec == 4)
-        p[i] = v[i];
-      else
-        p[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-    }
+}
+template <typename T>
+__device__ __forceinline__ typename T::vec zero_vec() {
+  if constexpr (T::kVec == 1)
+    return 0;
+  else
+    return vec4{0, 0, 0, 0};
 }
 
-// Stores kVec fp32 values of one lane as elements of type To; for a bf16
-// input with an fp32 output that is two vectors.
-template <typename To, int N, bool NT = false>
-__device__ __forceinline__ void store_vals(typename To::raw* p, const float* f, uint32_t left) {
-#pragma unroll
-  for (int i = 0; i < N; i += To::kVec) {
-    if constexpr (N < To::kVec) {
-      // fp32 lanes (4 values) into bf16: half a vector
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if ((uint32_t)j < left) p[j] = To::narrow(f[j]);
-    } else {
-      if ((uint32_t)i < left) store_vec<To, NT>(p + i, To::pack(f + i), left - i);
-    }
-  }
-}
-template <typename Ti, int N>
-__device__ __forceinline__ void load_vals(const typename Ti::raw* p, float* f, uint32_t left) {
-  if constexpr (N < Ti::kVec) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = (uint32_t)j < left ? Ti::widen(p[j]) : 0.0f;
+// The N (1, 4 or 8) fp32 values of a lane as N elements of To (F32 or BF16).
+template <typename To, int N>
+__device__ __forceinline__ void store_vals(typename To::raw* p, const float* f) {
+  if constexpr (N == 1) {
+    *p = To::narrow(f[0]);
+  } else if constexpr (N < To::kVec) {
+    typedef uint32_t vec2_u __attribute__((ext_vector_type(2), aligned(2)));
+    *reinterpret_cast<vec2_u*>(p) = vec2_u{BF16::pair(f[0], f[1]), BF16::pair(f[2], f[3])};
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += Ti::kVec) {
-      const vec4 v = (uint32_t)i < left ? load_vec<Ti>(p + i, left - i) : vec4{0, 0, 0, 0};
-      Ti::unpack(v, f + i);
-    }
+    for (int i = 0; i < N; i += To::kVec) store_vec<To>(p + i, To::pack(f + i));
   }
+}
+
+// A span of zeroes, `bytes` (a multiple of 2) from p on, by `lanes` lanes.
+__device__ __forceinline__ void zero_span(char* p, uint64_t bytes, uint32_t lane, uint32_t lanes) {
+  if (bytes < 16) {
+    if (lane < bytes / 2) reinterpret_cast<uint16_t*>(p)[lane] = 0;
+    return;
+  }
+  for (uint64_t i = lane * 16; i < bytes; i += lanes * 16)
+    *reinterpret_cast<vec4_u*>(p + (i + 16 <= bytes ? i : bytes - 16)) = vec4{0, 0, 0, 0};
 }
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 63u; }
