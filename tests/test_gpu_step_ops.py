@@ -258,6 +258,10 @@ GRADS = [
     (20_000, 70_001, 40, "falling", 0, torch.int64, 5),
     (70_000, 2_000_003, 3, "any", 0, torch.int32, None),
     (140_000, 600, 600, "falling", 0, torch.int32, None),
+    # tables too large to be zeroed beside the sort; a sort whose tiles hold more than four items a lane
+    (500, 40_000, 520, "falling", 0, torch.int64, None),
+    (5000, 150_000, 400, "outside", 0, torch.int64, None),
+    (300_001, 5000, 9, "falling", 0, torch.int32, None),
 ]
 
 
@@ -329,6 +333,26 @@ def test_embedding_grad_against_differences():
             assert abs(loss(x) - base - float(dw[v, d])) <= 4 * n * U * mag
 
 
+@pytest.mark.parametrize("n", [90, 6000])
+def test_masked_tokens_may_hold_anything(n):
+    """Gradients of tokens outside the table or of the padding id are not read
+    into any row, whatever they hold."""
+    g = gen(15)
+    vocab, dim = 50, 33
+    ids = torch.randint(-20, vocab + 20, (n,), generator=g, device="cuda")
+    dout = torch.randn((n, dim), generator=g, device="cuda")
+    out = (ids < 0) | (ids >= vocab) | (ids == 7)
+    ws = space(hc.hc_embedding_grad_workspace_bytes(n, vocab, dim))
+    got = []
+    for junk in (0.0, math.nan, math.inf):
+        dout[out] = junk
+        dw = torch.full((vocab, dim), GUARD, device="cuda")
+        hc.hc_embedding_grad(ids, dout, dw, ws, padding_id=7)
+        got.append(dw)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    assert not bool(got[0][7].any())
+
+
 def test_embedding_offsets_past_2_to_32():
     g = gen(14)
     vocab, dim, stride = 20, 70, 1 << 28
@@ -363,6 +387,8 @@ EXPERTS = [
     (5003, 2, 8, 32, 1031, 8, 0),
     (4096, 5, 3, 7, 72, 9, 3),
     (33_000, 4, 129, 1, 24, 129, 0),
+    (90_001, 4, 300, 3, 5, 300, 0),
+    (50, 2, 4, 1000, 40, 4, 0),
 ]
 
 
