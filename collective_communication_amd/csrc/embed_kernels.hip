@@ -93,11 +93,16 @@ __device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
 
 // ---------------------------------------------------------------- sorting the ids
 
-constexpr uint32_t kRankMax = 4096;     // ids sorted by counting smaller ones, in one launch
+// Ids up to this many are sorted in one launch: each workgroup places 64 ids,
+// its 16 waves comparing them with a sixteenth of all ids each.  n^2
+// comparisons, 2 instructions each, beat the launches of a radix sort while n
+// is small: up to 8192 where that takes two digits (the whole gradient of 8000
+// tokens x 256 bf16 into 5000 rows 24.0 us so, 27.3 by digits; of 10000, 27.7
+// and 27.8), up to 4096 where one digit does (into 500 rows, 6000 tokens 20.4
+// and 18.4).
+constexpr uint32_t kRankMax = 8192;
+inline bool by_rank(size_t n, size_t nkeys) { return n <= (nkeys <= kMaxRadix ? kRankMax / 2 : kRankMax); }
 
-// Each workgroup places 64 ids: its 16 waves compare them with a sixteenth of
-// all ids each.  n^2 comparisons, 2 instructions each, beat the launches of a
-// radix sort while n is small.
 __global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint32_t n, uint32_t* keys, uint32_t* pos,
                                                             uint32_t groups, ZeroJob zero) {
   if (blockIdx.x >= groups) {
@@ -206,8 +211,7 @@ __global__ void __launch_bounds__(kSortThreads) pass_scatter_kernel(Pass p, Zero
 constexpr size_t kHistBytes = (size_t)kMaxTiles * kMaxRadix * sizeof(uint32_t);
 
 size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
-  (void)nkeys;
-  return n <= kRankMax ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
+  return by_rank(n, nkeys) ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
 }
 
 namespace {
@@ -223,7 +227,7 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
     zero->done += beside;
     beside = (uint32_t)(zero->pieces - zero->done < kPiecesBeside ? zero->pieces - zero->done : kPiecesBeside);
   };
-  if (n <= kRankMax) {
+  if (by_rank(n, src.nkeys)) {
     const uint32_t groups = (uint32_t)((n + 63) / 64);
     next();
     rank_kernel<<<groups + beside, kSortThreads, 0, stream>>>(src, (uint32_t)n, keys, pos, groups, *zero);

@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(kSortThreads) expert_histogram_kernel(Sort s) 
                  s.hist + (size_t)blockIdx.x * s.experts);
 }
 
-// ONE: a single tile, which counts for itself (no histogram launch).
-template <bool ONE>
+// SELF: a short input, which every workgroup counts for itself (no histogram launch).
+template <bool SELF>
 __global__ void __launch_bounds__(kSortThreads) expert_scatter_kernel(Sort s) {
   __shared__ uint32_t counts[kSortWaves * kMaxRadix];
   __shared__ uint32_t scan[kSortWaves];
@@ -57,19 +57,11 @@ __global__ void __launch_bounds__(kSortThreads) expert_scatter_kernel(Sort s) {
   const uint32_t e = threadIdx.x;
   auto digit = [&](size_t i) { return load_key(s.src, i); };
   const Run run = load_run(lo, hi, s.tile, digit);
-  uint32_t before = 0, total = 0, used;
-  if constexpr (ONE) {
-    for (uint32_t d = threadIdx.x; d < s.experts; d += kSortThreads) counts[d] = 0;
-    __syncthreads();
-#pragma unroll
-    for (uint32_t k = 0; k < kHeld; ++k)       // a single tile is all held
-      if (run.held[k] != kNoKey) atomicAdd(&counts[run.held[k]], 1u);
-    __syncthreads();
-    total = e < s.experts ? counts[e] : 0;
-    __syncthreads();
-  } else {
+  uint32_t before, total, used;
+  if constexpr (SELF)
+    self_sums(counts, s.experts, s.n, lo, e, digit, &before, &total);
+  else
     tile_sums(s.hist, s.experts, s.tiles, blockIdx.x, e, &before, &total);
-  }
   const uint32_t padded = (total + s.align - 1) / s.align * s.align;
   const uint32_t first = block_scan(padded, scan, &used);
   if (blockIdx.x == 0) {
@@ -327,8 +319,7 @@ Rows rows_of(const hc_expert_plan_t& plan, size_t dim) {
 }  // namespace
 
 size_t expert_sort_ws_bytes(size_t nslots, size_t nexperts) {
-  const size_t tiles = sort_tiles(nslots);
-  return tiles <= 1 ? 0 : tiles * nexperts * sizeof(uint32_t);
+  return nslots <= kSelfCount ? 0 : sort_tiles(nslots) * nexperts * sizeof(uint32_t);
 }
 
 hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan, void* ws, hipStream_t stream) {
@@ -347,8 +338,8 @@ hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan
   s.slot_of_row = plan.slot_of_row;
   s.offsets = plan.expert_offsets;
   s.counts = plan.expert_counts;
-  if (s.tiles <= 1) {
-    expert_scatter_kernel<true><<<1, kSortThreads, 0, stream>>>(s);
+  if (s.n <= kSelfCount) {
+    expert_scatter_kernel<true><<<s.tiles ? s.tiles : 1, kSortThreads, 0, stream>>>(s);
     return hipGetLastError();
   }
   expert_histogram_kernel<<<s.tiles, kSortThreads, 0, stream>>>(s);

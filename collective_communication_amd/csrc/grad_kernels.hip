@@ -413,7 +413,7 @@ hipError_t make_plan(const void* const* grads, void* const* outs, const size_t* 
   }
   p->chunks = (uint32_t)chunks;
   p->grid = p->chunks < kMaxGrid ? p->chunks : kMaxGrid;
-  p->by_args = p->n <= kBatch && p->chunks <= kMaxGrid;
+  p->by_args = p->n <= kBatch;
   Entry* table = reinterpret_cast<Entry*>(static_cast<char*>(ws) + kPartialBytes);
   uint32_t* firsts = reinterpret_cast<uint32_t*>(table + p->n);
   p->view = TableView{table, firsts};

@@ -252,6 +252,8 @@ GRADS = [
     (500, 33, 1031, "falling", 100, torch.int32, 100),
     (4096, 300, 24, "falling", 0, torch.int64, None),
     (4097, 300, 24, "falling", 0, torch.int64, 1),
+    (8192, 1025, 24, "falling", 0, torch.int64, None),
+    (8193, 1025, 24, "outside", 5, torch.int32, None),
     (5000, 2, 72, "one", 0, torch.int32, None),
     (5000, 9, 520, "none", 0, torch.int32, None),
     (9001, 1500, 130, "outside", -700, torch.int64, None),
