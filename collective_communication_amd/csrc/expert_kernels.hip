@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_scatter_kernel(Sort s) {
   const Run run = load_run(lo, hi, s.tile, digit);
   uint32_t before, total, used;
   if constexpr (SELF)
-    self_sums(counts, s.experts, s.n, lo, e, digit, &before, &total);
+    self_sums(counts, s.experts, s.n, lo, run, e, digit, &before, &total);
   else
     tile_sums(s.hist, s.experts, s.tiles, blockIdx.x, e, &before, &total);
   const uint32_t padded = (total + s.align - 1) / s.align * s.align;

@@ -86,52 +86,23 @@ __device__ __forceinline__ void tile_histogram(uint32_t* lds, uint32_t radix, si
 }
 
 // Per digit: the sum of the tiles' counts before `tile`, and over all tiles.
-// All loads of 32 tiles are in flight at once.
+// All tiles' loads are in flight at once.
 __device__ __forceinline__ void tile_sums(const uint32_t* hist, uint32_t radix, uint32_t tiles, uint32_t tile,
                                           uint32_t d, uint32_t* before, uint32_t* total) {
   uint32_t b = 0, a = 0;
   if (d < radix) {
-    for (uint32_t t0 = 0; t0 < tiles; t0 += 32) {
-      uint32_t c[32];
+    uint32_t c[kMaxTiles];
 #pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) c[i] = t0 + i < tiles ? hist[(size_t)(t0 + i) * radix + d] : 0;
-      __builtin_amdgcn_sched_barrier(0);
+    for (uint32_t i = 0; i < kMaxTiles; ++i) c[i] = i < tiles ? hist[(size_t)i * radix + d] : 0;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) {
-        b += t0 + i < tile ? c[i] : 0;
-        a += c[i];
-      }
+    for (uint32_t i = 0; i < kMaxTiles; ++i) {
+      b += i < tile ? c[i] : 0;
+      a += c[i];
     }
   }
   *before = b;
   *total = a;
-}
-
-// The same two sums, counted by the workgroup itself from all n items: up to
-// kSelfCount items that is less than a histogram launch before it (sort and
-// dispatch of 500 tokens x 8 slots 9.2 us so, 9.8 by two launches; of 2000 x 8,
-// 13.1 and 11.2).  counts: 2 x radix words of LDS, free again afterwards.
-constexpr uint32_t kSelfCount = 4096;
-template <typename Digit>
-__device__ __forceinline__ void self_sums(uint32_t* counts, uint32_t radix, size_t n, size_t lo, uint32_t d,
-                                          Digit digit, uint32_t* before, uint32_t* total) {
-  for (uint32_t i = threadIdx.x; i < 2 * radix; i += kSortThreads) counts[i] = 0;
-  __syncthreads();
-  for (size_t i0 = 0; i0 < n; i0 += 8 * kSortThreads) {
-    uint32_t key[8];
-#pragma unroll
-    for (uint32_t u = 0; u < 8; ++u) {
-      const size_t i = i0 + u * kSortThreads + threadIdx.x;
-      key[u] = i < n ? digit(i) : kNoKey;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < 8; ++u)
-      if (key[u] != kNoKey) atomicAdd(&counts[(i0 + u * kSortThreads < lo ? 0 : radix) + key[u]], 1u);
-  }
-  __syncthreads();
-  *before = d < radix ? counts[d] : 0;
-  *total = d < radix ? *before + counts[radix + d] : 0;
-  __syncthreads();
 }
 
 // A wave's items of its tile: a contiguous run, 64 at a time.  The first
@@ -156,6 +127,35 @@ __device__ __forceinline__ Run load_run(size_t lo, size_t hi, uint32_t tile_item
   return r;
 }
 
+// The same two sums, counted by the workgroup itself from all n items: up to
+// kSelfCount items that is less than a histogram launch before it (sort and
+// dispatch of 500 tokens x 8 slots 9.2 us so, 9.8 by two launches; of 2000 x 8,
+// 13.1 and 11.2).  counts: 2 x radix words of LDS, free again afterwards.
+constexpr uint32_t kSelfCount = 4096;
+template <typename Digit>
+__device__ __forceinline__ void self_sums(uint32_t* counts, uint32_t radix, size_t n, size_t lo, const Run& run,
+                                          uint32_t d, Digit digit, uint32_t* before, uint32_t* total) {
+  for (uint32_t i = threadIdx.x; i < 2 * radix; i += kSortThreads) counts[i] = 0;
+  __syncthreads();
+  const bool one = n <= kMinTile;       // all items are the run's first round
+  if (one && run.held[0] != kNoKey) atomicAdd(&counts[radix + run.held[0]], 1u);
+  for (size_t i0 = one ? n : 0; i0 < n; i0 += 8 * kSortThreads) {
+    uint32_t key[8];
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u) {
+      const size_t i = i0 + u * kSortThreads + threadIdx.x;
+      key[u] = i < n ? digit(i) : kNoKey;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u)
+      if (key[u] != kNoKey) atomicAdd(&counts[(i0 + u * kSortThreads < lo ? 0 : radix) + key[u]], 1u);
+  }
+  __syncthreads();
+  *before = d < radix ? counts[d] : 0;
+  *total = d < radix ? *before + counts[radix + d] : 0;
+  __syncthreads();
+}
+
 // Hands each item of the run its place: put(i, digit, place) with place = the
 // digit's first place for this tile (my_base, of digit threadIdx.x) + how many
 // items of the tile before it have the same digit.  counts: kSortWaves x radix
@@ -176,12 +176,13 @@ __device__ __forceinline__ void place_items(uint32_t* counts, uint32_t radix, ui
   }
   __syncthreads();
   if (threadIdx.x < radix) {
-    uint32_t p = my_base;
+    uint32_t c[kSortWaves], p = my_base;
+#pragma unroll
+    for (uint32_t v = 0; v < kSortWaves; ++v) c[v] = counts[v * radix + threadIdx.x];
 #pragma unroll
     for (uint32_t v = 0; v < kSortWaves; ++v) {
-      const uint32_t c = counts[(size_t)v * radix + threadIdx.x];
-      counts[(size_t)v * radix + threadIdx.x] = p;
-      p += c;
+      counts[v * radix + threadIdx.x] = p;
+      p += c[v];
     }
   }
   __syncthreads();
