@@ -264,6 +264,7 @@ GRADS = [
     (500, 40_000, 520, "falling", 0, torch.int64, None),
     (5000, 150_000, 400, "outside", 0, torch.int64, None),
     (300_001, 5000, 9, "falling", 0, torch.int32, None),
+    (400_003, 100, 10, "one", 0, torch.int32, None),
 ]
 
 
