@@ -4,14 +4,21 @@
 //   out[t]     = round(scale * weight[key_t])          zero where t has no key
 //   dweight[v] = round(scale * sum_{t: key_t = v} dout[t])
 //
-// The lookup streams rows.  The gradient never adds with atomics: the ids are
+// Both are bound by memory.  The gradient never adds with atomics: the ids are
 // sorted (stable), the sorted list is cut into chunks of C tokens, and a wave
 // sums one chunk's rows over 64 vectors of columns, writing each run of equal
 // keys that lies inside the chunk straight to its row.  A run that crosses a
 // chunk's edge leaves fp32 partials, which a second launch adds in order; so
 // a token that fills half the batch is spread over as many waves as its
-// chunks.  Rows without a token are zeroed by further waves of the first
-// launch, each of which looks 16 rows up in the sorted list.
+// chunks.  Rows without a token are zeroed beside all of that: the table's
+// first rows beside the sort's launches, the others by further workgroups of
+// the sum and join launches, which look their rows up in the sorted list.
+//
+// Measured: the lookup of 30,011 x 4096 bf16, a quarter of them in the table,
+// 40 us (246 MB written, 7.5 TB/s); the gradient of 32,768 x 2048 bf16 into
+// 100,003 fp32 rows 198-205 us, of which the sort 24 (45 with 200 MB zeroed
+// beside it): 1.0 GB in all, 0.85 of it written, 5.0 TB/s, as a large copy
+// does.  Its parts alone: the sums 60-75 us, all the zeroing 117 us.
 #include "key_sort.hpp"
 #include "launch.hpp"
 
@@ -28,7 +35,8 @@ inline uint32_t blocks_for(uint64_t waves) {
 // ---------------------------------------------------------------- lookup
 
 // A wave handles 64 >> lg rows of 1 << lg vectors (lg < 6: narrow tables), or
-// a slice of U * 64 vectors of one row (lg == 6).
+// a slice of U * 64 vectors of one row (lg == 6).  Plain loads: a frequent
+// token's row comes out of the cache (non-temporal ones 56 against 41 us).
 template <typename T, int U, bool NT>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size_t ntokens, const void* weight,
                                                              uint32_t dim, size_t wstride, float scale, void* out,
@@ -69,7 +77,9 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
 // and depend on nothing but the ids; the other compute units meanwhile zero
 // the first rows of the table, tokens or not (the sums come later and write
 // theirs again).  Pieces of some 64 KB: of one flat range where the rows are
-// contiguous, else whole rows.
+// contiguous, else whole rows.  A launch of the sort takes 2-3 us longer for 25
+// MB of them and 5 us for 50 MB, which alone would take 8 (2000 tokens x 1000
+// fp32 into 10,007 rows, 40 MB: 23.4 us without, 18.3 with).
 constexpr uint64_t kPieceBytes = 65536;
 
 struct ZeroJob {
@@ -230,9 +240,9 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
   if (by_rank(n, src.nkeys)) {
     const uint32_t groups = (uint32_t)((n + 63) / 64);
     next();
-    rank_kernel<<<groups + beside, kSortThreads, 0, stream>>>(src, (uint32_t)n, keys, pos, groups, *zero);
+    HC_ENQUEUE(rank_kernel, groups + beside, kSortThreads, stream, src, (uint32_t)n, keys, pos, groups, *zero);
     zero->done += beside;
-    return hipGetLastError();
+    return hipSuccess;
   }
   uint32_t bits = 1;
   while (bits < 32 && ((uint64_t)src.nkeys - 1) >> bits) ++bits;
@@ -248,11 +258,9 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
     p.keys_out = last_buffer ? keys : tmp_keys;
     p.pos_out = last_buffer ? pos : tmp_pos;
     next();
-    pass_histogram_kernel<<<p.tiles + beside, kSortThreads, 0, stream>>>(p, *zero);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    HC_ENQUEUE(pass_histogram_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
     next();
-    pass_scatter_kernel<<<p.tiles + beside, kSortThreads, 0, stream>>>(p, *zero);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    HC_ENQUEUE(pass_scatter_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
     p.keys = p.keys_out;
     p.pos = p.pos_out;
   }
@@ -267,6 +275,7 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
 namespace {
 
 constexpr size_t kZeroBytes = 32768;    // of table rows per zeroing workgroup, 4 to 64 rows
+                                        // (64 and 128 KB: 1-3% slower)
 constexpr uint32_t kJoinCols = 256;     // columns per workgroup and round of the join: 4 fp32 per lane
 
 struct Grad {
@@ -537,8 +546,9 @@ GradLayout grad_layout(size_t n, size_t vocab, size_t dim) {
 
 template <typename Ti, typename To, bool ACC>
 hipError_t run_grad(Grad g, hipStream_t stream) {
-  // A share of the zeroing runs beside the joins, which by themselves are a
-  // few workgroups waiting for memory.
+  // A quarter of the zeroing that is left runs beside the joins, which by
+  // themselves are a few workgroups waiting for memory (a half or all of it
+  // there: the same within 3%).
   const bool joins = g.nchunks > 1;
   g.slices = (g.dim + 64 * Ti::kVec - 1) / (64 * Ti::kVec);
   g.sum_units = (uint64_t)g.nchunks * g.slices;
@@ -548,9 +558,8 @@ hipError_t run_grad(Grad g, hipStream_t stream) {
   const uint32_t now = zero_blocks - later, sum_blocks = (uint32_t)((g.sum_units + kWaves - 1) / kWaves);
   const uint64_t blocks = (uint64_t)sum_blocks + now;
   if (blocks) {
-    grad_kernel<Ti, To, ACC><<<(uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks), kThreads, 0, stream>>>(
-        g, sum_blocks, now);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    HC_ENQUEUE((grad_kernel<Ti, To, ACC>), (uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks), kThreads, stream, g,
+               sum_blocks, now);
   }
   if (!joins) return hipSuccess;
   const uint32_t cols = (g.dim + kJoinCols - 1) / kJoinCols, col_blocks = cols < 8 ? cols : 8;
@@ -559,8 +568,8 @@ hipError_t run_grad(Grad g, hipStream_t stream) {
   g.join_chunks = all >= 2048 * 8 ? 8 : all <= 2048 ? 1 : (uint32_t)(all / 2048);
   const uint32_t groups = (g.nchunks - 1 + g.join_chunks - 1) / g.join_chunks;
   const uint32_t join_blocks = (groups < 65536 ? groups : 65536) * col_blocks;
-  join_kernel<To, ACC><<<join_blocks + later, kThreads, 0, stream>>>(g, join_blocks, col_blocks, now);
-  return hipGetLastError();
+  HC_ENQUEUE((join_kernel<To, ACC>), join_blocks + later, kThreads, stream, g, join_blocks, col_blocks, now);
+  return hipSuccess;
 }
 
 }  // namespace
@@ -576,9 +585,9 @@ hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* we
     const uint32_t slices = (nvec + 64 * U - 1) / (64 * U);
     const uint64_t units = (uint64_t)((ntokens + (64u >> lg) - 1) / (64u >> lg)) * slices;
     auto launch = [&](auto kernel) {
-      kernel<<<blocks_for(units), kThreads, 0, stream>>>(src, ntokens, weight, (uint32_t)dim, wstride, scale, out,
-                                                         ostride, lg, slices, units);
-      return hipGetLastError();
+      HC_ENQUEUE(kernel, blocks_for(units), kThreads, stream, src, ntokens, weight, (uint32_t)dim, wstride, scale, out,
+                 ostride, lg, slices, units);
+      return hipSuccess;
     };
     return ntokens * dim * sizeof(typename T::raw) >= kStreamStoreBytes ? launch(embedding_kernel<T, U, true>)
                                                                         : launch(embedding_kernel<T, U, false>);
@@ -587,7 +596,9 @@ hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* we
   return dim < BF16::kVec ? run(BF16S{}) : run(BF16{});
 }
 
-size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) { return grad_layout(ntokens, vocab, dim).bytes; }
+size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) {
+  return grad_layout(ntokens, vocab, dim).bytes;
+}
 
 hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const void* dout, hc_dtype_t dtype, size_t dim,
                                  size_t dstride, float scale, void* dweight, hc_dtype_t dwtype, size_t wstride,
@@ -628,7 +639,9 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
                           : zero.flat              ? zero.done * kPieceBytes / row_bytes
                                                    : zero.done * zero.rows_per_piece;
   g.zero_from = accumulate ? g.vocab : (uint32_t)zeroed;
-  g.zero_rows = row_bytes >= kZeroBytes / 4 ? 4 : row_bytes <= kZeroBytes / 64 ? 64 : (uint32_t)(kZeroBytes / row_bytes);
+  g.zero_rows = row_bytes >= kZeroBytes / 4    ? 4
+                : row_bytes <= kZeroBytes / 64 ? 64
+                                               : (uint32_t)(kZeroBytes / row_bytes);
   auto run = [&](auto in, auto table) {
     typedef decltype(in) Ti;
     typedef decltype(table) To;

@@ -9,8 +9,9 @@
 // All but the sort are streams over rows, organised by token: a wave reads a
 // token's slice once and writes its k copies, or reads its k rows and writes
 // one sum, so the side that is k times larger moves exactly once and the
-// other is not read k times over.  Sums run over j in order within a lane:
-// no atomics.  The token's row numbers are loaded once into the wave's lanes
+// other is not read k times over.  (By row instead, gathering each row's
+// token: 298 against 232 us for 16,384 x 8 rows of 4096 bf16.)  Sums run over j
+// in order within a lane: no atomics.  The token's row numbers are loaded once into the wave's lanes
 // and read from there as scalars, so every row's address is scalar.
 #include <type_traits>
 
@@ -124,6 +125,10 @@ __device__ __forceinline__ void zero_padding(const Rows& r, uint64_t unit) {
 }
 
 // A wave copies a slice of U * 64 vectors of one token to its k rows.
+// Measured, 16,384 tokens x 8 of 128 experts x 4096 bf16, rows padded to 32:
+// 240 us for 1.23 GB, 5.1 TB/s; a probe that does nothing else takes 225-232 with
+// its input out of memory, and writing the rows alone takes 187.  U = 1 or 4:
+// 251 and 250 where 2 took 247.
 template <typename T, int U, bool NT>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
   const uint32_t lane = lane_id();
@@ -157,6 +162,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
 }
 
 // A wave sums a slice of 64 vectors of one token's rows, four rows in flight.
+// Measured: 5003 tokens x 2 slots x 1031 fp32 11.4 us (62 MB); 16,384 x 8 x 4096
+// bf16 210 us (1.2 GB, 5.8 TB/s), eight rows in flight 204 there and 2-10% more
+// than four on small inputs.
 template <typename T, bool WEIGHTED, bool NTL, bool NT>
 __global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
   constexpr int N = T::kVec, J = 4;
@@ -339,13 +347,12 @@ hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan
   s.offsets = plan.expert_offsets;
   s.counts = plan.expert_counts;
   if (s.n <= kSelfCount) {
-    expert_scatter_kernel<true><<<s.tiles ? s.tiles : 1, kSortThreads, 0, stream>>>(s);
-    return hipGetLastError();
+    HC_ENQUEUE(expert_scatter_kernel<true>, s.tiles ? s.tiles : 1, kSortThreads, stream, s);
+    return hipSuccess;
   }
-  expert_histogram_kernel<<<s.tiles, kSortThreads, 0, stream>>>(s);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  expert_scatter_kernel<false><<<s.tiles, kSortThreads, 0, stream>>>(s);
-  return hipGetLastError();
+  HC_ENQUEUE(expert_histogram_kernel, s.tiles, kSortThreads, stream, s);
+  HC_ENQUEUE(expert_scatter_kernel<false>, s.tiles, kSortThreads, stream, s);
+  return hipSuccess;
 }
 
 hipError_t launch_expert_dispatch(const void* x, hc_dtype_t dtype, size_t dim, size_t xstride,
@@ -364,10 +371,10 @@ hipError_t launch_expert_dispatch(const void* x, hc_dtype_t dtype, size_t dim, s
     const uint32_t blocks = blocks_for(r.units);
     // the rows in use number at most ntokens * k and the padding
     if (r.ntokens * r.k * r.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
-      dispatch_kernel<T, U, true><<<blocks, kThreads, 0, stream>>>(r);
+      HC_ENQUEUE((dispatch_kernel<T, U, true>), blocks, kThreads, stream, r);
     else
-      dispatch_kernel<T, U, false><<<blocks, kThreads, 0, stream>>>(r);
-    return hipGetLastError();
+      HC_ENQUEUE((dispatch_kernel<T, U, false>), blocks, kThreads, stream, r);
+    return hipSuccess;
   });
 }
 
@@ -386,8 +393,8 @@ hipError_t launch_expert_combine(const void* rows, hc_dtype_t dtype, size_t dim,
     r.units = (uint64_t)r.ntokens * r.slices;
     if (!r.units) return hipSuccess;
     auto launch = [&](auto kernel) {
-      kernel<<<blocks_for(r.units), kThreads, 0, stream>>>(r);
-      return hipGetLastError();
+      HC_ENQUEUE(kernel, blocks_for(r.units), kThreads, stream, r);
+      return hipSuccess;
     };
     const size_t bytes = r.ntokens * r.dim * sizeof(typename T::raw);
     const bool nts = bytes >= kStreamStoreBytes, ntl = bytes * r.k >= kStreamLoadBytes;
@@ -408,12 +415,12 @@ static hipError_t run_combine_grad(Rows r, hipStream_t stream) {
   const size_t bytes = r.ntokens * r.k * r.dim * sizeof(typename T::raw);
   static_assert(kStreamLoadBytes >= kStreamStoreBytes, "streamed rows have streamed gradients");
   if (bytes >= kStreamLoadBytes)
-    combine_grad_kernel<T, WPT, true, true><<<blocks, WPT * 64, 0, stream>>>(r);
+    HC_ENQUEUE((combine_grad_kernel<T, WPT, true, true>), blocks, WPT * 64, stream, r);
   else if (bytes >= kStreamStoreBytes)
-    combine_grad_kernel<T, WPT, false, true><<<blocks, WPT * 64, 0, stream>>>(r);
+    HC_ENQUEUE((combine_grad_kernel<T, WPT, false, true>), blocks, WPT * 64, stream, r);
   else
-    combine_grad_kernel<T, WPT, false, false><<<blocks, WPT * 64, 0, stream>>>(r);
-  return hipGetLastError();
+    HC_ENQUEUE((combine_grad_kernel<T, WPT, false, false>), blocks, WPT * 64, stream, r);
+  return hipSuccess;
 }
 template <typename T>
 static hipError_t run_combine_grad(const Rows& r, hipStream_t stream) {

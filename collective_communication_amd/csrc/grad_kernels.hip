@@ -6,15 +6,24 @@
 // Both are streams over memory: the norm reads every element once, clipping
 // reads it again and writes it.  The tensors are cut into chunks of 16 KB,
 // numbered through all tensors, so that one launch covers a thousand small
-// vectors and a large matrix evenly; a chunk's tensor is found by a binary
-// search over the tensors' first chunks.  The table of tensors travels in the
-// kernel's own arguments (up to kBatch tensors) or in the workspace, which a
-// launch per kBatch tensors fills; no host memory has to outlive the call.
+// vectors and a large matrix evenly; a chunk's tensor is found by a search
+// over the tensors' first chunks.  The table of tensors travels in the kernel's
+// own arguments (up to kBatch tensors) or in the workspace, which a launch per
+// kPacked tensors fills; no host memory has to outlive the call.
 //
 // Squares are summed in fp64: a product of two fp32 values is exact there and
 // can neither overflow nor vanish, and the sum's rounding stays far below the
-// result's.  Each workgroup leaves one partial; the partials are added in a
-// fixed order, by the clipping kernel's workgroups themselves.
+// result's; it costs nothing, since the pass waits for memory either way (1 GiB
+// summed in 153 us with fp64, 151 with fp32).  Each workgroup leaves one
+// partial; they are added in a fixed order, by the clipping launch's own
+// workgroups up to 128 MB of gradients, by a launch between the two above.
+//
+// Measured on 2^29 bf16 values in 450 tensors, outputs at odd elements: norm
+// 162 us (6.6 TB/s; plain loads 172-210), clipping 350-360 us (6.0 TB/s;
+// persistent workgroups with plain stores 430); 525 us a call.  2^25 values in
+// 290 tensors, mixed types: 16 + 27 us, 48 us a call.  A sum by whichever
+// workgroup ends last, behind agent-scope atomics, took the norm pass from 19
+// to 96 us.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "step_launch.hpp"
@@ -26,7 +35,10 @@ constexpr uint32_t kChunkBytes = 16384;
 constexpr uint32_t kVecs = kChunkBytes / 16 / kThreads;   // 16-byte vectors per lane and chunk
 constexpr uint32_t kBatch = 128;        // tensors per kernel argument: 3.6 KB of the 4 KB
 constexpr uint32_t kMaxGrid = 2048;     // 8 workgroups of 4 waves on each of 256 CUs
+constexpr uint32_t kMostBlocks = 1u << 23;   // of a launch: its lanes are counted in 32 bits
 constexpr uint32_t kStreamChunks = (uint32_t)(kStreamStoreBytes / kChunkBytes);
+// Up to here the clipping launch has at most kMaxGrid workgroups, which add the
+// partials up themselves; above it has one per chunk.
 constexpr uint32_t kFuseChunks = (128u << 20) / kChunkBytes;
 constexpr uint64_t kBf16Bit = 1ull << 63;
 
@@ -44,7 +56,7 @@ struct Batch {
 // begins up to a line before the tensor), so that a wave's stores fill whole
 // lines however the output lies; loads may straddle lines, stores must not:
 // with outputs at odd elements the clipping of 2^29 bf16 values took 385 us
-// on chunks counted from the tensor's start and takes 340 on these.
+// on chunks counted from the tensor's start and takes 350-360 on these.
 __host__ __device__ __forceinline__ uint32_t lead_bytes(const void* p) { return (uint32_t)((uintptr_t)p & 127u); }
 __host__ __device__ __forceinline__ uint64_t chunks_of(const Entry& e) {
   const uint64_t bytes = (e.count & ~kBf16Bit) * (e.count & kBf16Bit ? 2 : 4);
@@ -433,8 +445,7 @@ hipError_t make_plan(const void* const* grads, void* const* outs, const size_t* 
     }
     next += (uint32_t)chunks_of(x);
     if (!p->by_args && (k == kPacked || done + k == p->n)) {
-      table_kernel<<<1, kThreads, 0, stream>>>(pack, k, first, table + done, firsts + done);
-      if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      HC_ENQUEUE(table_kernel, 1, kThreads, stream, pack, k, first, table + done, firsts + done);
       done += k;
       first = next;
       k = 0;
@@ -446,35 +457,37 @@ hipError_t make_plan(const void* const* grads, void* const* outs, const size_t* 
 // The clipping launch; partials NULL: the norm is in *norm already.
 template <bool INF>
 hipError_t run_clip(const Plan& p, float max_norm, float* norm, const double* partials, hipStream_t stream) {
-  const uint32_t grid = partials ? p.grid : p.chunks;
+  const uint32_t grid = partials ? p.grid : p.chunks < kMostBlocks ? p.chunks : kMostBlocks;
   const uint32_t np = partials ? p.grid : 0;
   const bool nt = p.chunks >= kStreamChunks;
   if (p.by_args) {
     if (nt)
-      clip_args_kernel<INF, true><<<grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials, np, norm, max_norm);
+      HC_ENQUEUE((clip_args_kernel<INF, true>), grid, kThreads, stream, p.batch, p.n, p.chunks, partials, np, norm,
+                 max_norm);
     else
-      clip_args_kernel<INF, false><<<grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials, np, norm, max_norm);
+      HC_ENQUEUE((clip_args_kernel<INF, false>), grid, kThreads, stream, p.batch, p.n, p.chunks, partials, np, norm,
+                 max_norm);
   } else {
     if (nt)
-      clip_table_kernel<INF, true><<<grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials, np, norm, max_norm);
+      HC_ENQUEUE((clip_table_kernel<INF, true>), grid, kThreads, stream, p.view, p.n, p.chunks, partials, np, norm,
+                 max_norm);
     else
-      clip_table_kernel<INF, false><<<grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials, np, norm, max_norm);
+      HC_ENQUEUE((clip_table_kernel<INF, false>), grid, kThreads, stream, p.view, p.n, p.chunks, partials, np, norm,
+                 max_norm);
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 template <bool INF>
 hipError_t run(const Plan& p, bool clip, float max_norm, float* norm, double* partials, hipStream_t stream) {
   if (p.grid) {
     if (p.by_args)
-      norm_args_kernel<INF><<<p.grid, kThreads, 0, stream>>>(p.batch, p.n, p.chunks, partials);
+      HC_ENQUEUE(norm_args_kernel<INF>, p.grid, kThreads, stream, p.batch, p.n, p.chunks, partials);
     else
-      norm_table_kernel<INF><<<p.grid, kThreads, 0, stream>>>(p.view, p.n, p.chunks, partials);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      HC_ENQUEUE(norm_table_kernel<INF>, p.grid, kThreads, stream, p.view, p.n, p.chunks, partials);
   }
   if (clip && p.grid && p.chunks <= kFuseChunks) return run_clip<INF>(p, max_norm, norm, partials, stream);
-  finish_kernel<INF><<<1, kThreads, 0, stream>>>(partials, p.grid, norm);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  HC_ENQUEUE(finish_kernel<INF>, 1, kThreads, stream, partials, p.grid, norm);
   return clip && p.grid ? run_clip<INF>(p, max_norm, norm, nullptr, stream) : hipSuccess;
 }
 

@@ -33,7 +33,8 @@ inline uint32_t sort_tile(size_t n) {
 inline uint32_t sort_tiles(size_t n) { return (uint32_t)((n + sort_tile(n) - 1) / sort_tile(n)); }
 
 __device__ __forceinline__ uint32_t load_key(const KeySource& s, size_t i) {
-  const int64_t id = s.id_bytes == 8 ? static_cast<const int64_t*>(s.ids)[i] : (int64_t)static_cast<const int32_t*>(s.ids)[i];
+  const int64_t id =
+      s.id_bytes == 8 ? static_cast<const int64_t*>(s.ids)[i] : (int64_t)static_cast<const int32_t*>(s.ids)[i];
   // unsigned wrap-around: an id below start becomes a huge difference
   const uint64_t k = (uint64_t)id - (uint64_t)s.start;
   if (k >= s.nkeys || (s.use_skip && id == s.skip)) return kNoKey;

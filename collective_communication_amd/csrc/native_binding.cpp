@@ -46,7 +46,8 @@ hc_dtype_t dtype_of(const at::Tensor& t) {
 void* flat(PyObject* o, size_t need, const char* name, size_t* bytes = nullptr) {
   const at::Tensor& t = tensor(o, name);
   if (!t.is_cuda() || !t.is_contiguous()) raise(PyExc_ValueError, "%s must be a contiguous device tensor", name);
-  if ((size_t)t.numel() < need) raise(PyExc_ValueError, "%s holds %zd elements, needs %zu", name, (Py_ssize_t)t.numel(), need);
+  if ((size_t)t.numel() < need)
+    raise(PyExc_ValueError, "%s holds %zd elements, needs %zu", name, (Py_ssize_t)t.numel(), need);
   if (bytes) *bytes = t.nbytes();
   return t.data_ptr();
 }
@@ -63,7 +64,8 @@ struct Ids {
 };
 Ids ids_of(PyObject* o, const char* name) {
   const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong) raise(PyExc_TypeError, "%s must be int32 or int64", name);
+  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)
+    raise(PyExc_TypeError, "%s must be int32 or int64", name);
   return Ids{flat(o, 0, name), t.scalar_type() == at::kInt ? 4 : 8, (size_t)t.numel()};
 }
 

@@ -165,9 +165,7 @@ void log_plan(const char* op, const hc_expert_plan_t* p, size_t dim, hc_dtype_t 
 }
 
 hc_status_t done(hipError_t e, const char* where) {
-  if (e == hipSuccess) return HC_SUCCESS;
-  if (e == hipErrorInvalidValue) (void)hipGetLastError();
-  return device_fail(e, where);
+  return e == hipSuccess ? HC_SUCCESS : device_fail(e, where);
 }
 
 }  // namespace

@@ -11,6 +11,25 @@
 
 namespace hc {
 
+// Enqueues a kernel and returns that launch's own status: not whatever error
+// an earlier call of the process may have left behind.  The arguments are
+// converted to the kernel's parameter types.
+template <typename... P, typename... A>
+inline hipError_t enqueue(void (*kernel)(P...), uint32_t grid, uint32_t block, hipStream_t stream, const A&... args) {
+  static_assert(sizeof...(P) == sizeof...(A), "one argument per parameter");
+  return [&](const P&... p) {
+    const void* at[] = {static_cast<const void*>(&p)...};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(block),
+                                         const_cast<void**>(at), 0, stream);
+    if (e != hipSuccess) (void)hipGetLastError();   // reported here, so not once more by the next reader
+    return e;
+  }(args...);
+}
+#define HC_ENQUEUE(kernel, ...) \
+  do { \
+    if (hipError_t e_ = ::hc::enqueue(kernel, __VA_ARGS__); e_ != hipSuccess) return e_; \
+  } while (0)
+
 // ---- gradient norm and clipping (grad_kernels.hip)
 size_t grad_norm_ws_bytes(size_t ntensors);
 // norm of all tensors into *d_norm; when outs is not NULL, also outs[i] =
