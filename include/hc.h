@@ -1,7 +1,8 @@
 /*
  * hc.h -- C ABI of the MI355X (gfx950) emulated ring AllReduce data path and
  * the lossless bf16 exponent codecs, HCZ1 (fixed-length codes) and HCE1
- * (Huffman codes) (library: libhc.so).
+ * (Huffman codes), and of the operators around the exchange: gradient norm and
+ * clipping, embedding lookup and gradient, tokens by expert (library: libhc.so).
  *
  * The ring is emulated on ONE GPU: R "ranks" are R device buffers in the same
  * HBM; a hop's link transfer is the receiver reading the sender's buffer.  All
