@@ -95,6 +95,7 @@ struct Rows {
   const float* weights;
   size_t ntokens;
   uint32_t k, experts, dim, slices;
+  uint32_t rows_room;       // a row number outside of it counts as none
   const void* x;            // by token (dispatch), or dout
   size_t xstride;
   const void* rows;         // by row (combine, gradient)
@@ -113,7 +114,7 @@ constexpr uint32_t kPadRows = 4, kMaxPadUnits = 64;
 template <typename T, bool NT>
 __device__ __forceinline__ void zero_padding(const Rows& r, uint64_t unit) {
   const uint32_t e = (uint32_t)(unit / r.pad_units);
-  const uint32_t end = (uint32_t)r.offsets[e + 1];
+  const uint32_t end = min((uint32_t)r.offsets[e + 1], r.rows_room);
   for (uint32_t g = (uint32_t)(r.offsets[e] + r.counts[e]) + (uint32_t)(unit % r.pad_units) * kPadRows; g < end;
        g += r.pad_units * kPadRows) {
     for (uint32_t row = g; row < end && row < g + kPadRows; ++row) {
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(Rows r) {
     const size_t t = (u - r.padding) / r.slices;
     const uint32_t c0 = (uint32_t)((u - r.padding) % r.slices) * (U * 64 * T::kVec) + lane * T::kVec;
     const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
-    uint64_t there = __ballot(row >= 0);
+    uint64_t there = __ballot((uint32_t)row < r.rows_room);
     if (!there) continue;
     typename T::vec v[U];
 #pragma unroll
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Rows r) {
     const uint32_t c = (uint32_t)(u % r.slices) * (64 * N) + lane * N;
     const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
     const uint32_t w = WEIGHTED && lane < r.k ? f32_bits(r.weights[t * r.k + lane]) : f32_bits(1.0f);
-    uint64_t there = __ballot(row >= 0);
+    uint64_t there = __ballot((uint32_t)row < r.rows_room);
     const bool mine = c < r.dim;    // every lane stays, for the lane reads below
     const uint32_t at = vec_at<T>(c, r.dim);
     float acc[N];
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(WPT * 64) combine_grad_kernel(Rows r) {
     const size_t t = u - pad_blocks;
     const int32_t row = lane < r.k ? r.row_of_slot[t * r.k + lane] : -1;
     const uint32_t w = lane < r.k ? f32_bits(r.weights[t * r.k + lane]) : 0;
-    uint64_t there = __ballot(row >= 0);
+    uint64_t there = __ballot((uint32_t)row < r.rows_room);
     float dw = 0.0f;        // lane j: slot j's
     while (there) {
       float dot[J], g[J];
@@ -318,6 +319,7 @@ Rows rows_of(const hc_expert_plan_t& plan, size_t dim) {
   r.k = (uint32_t)plan.k;
   r.experts = (uint32_t)plan.nexperts;
   r.dim = (uint32_t)dim;
+  r.rows_room = (uint32_t)plan.rows;
   r.pad_units = ((uint32_t)plan.row_align - 1 + kPadRows - 1) / kPadRows;
   if (r.pad_units > kMaxPadUnits) r.pad_units = kMaxPadUnits;
   r.padding = (uint64_t)r.pad_units * r.experts;

@@ -633,6 +633,7 @@ hc_status_t hc_embedding_grad(const void *ids, int id_bytes, size_t ntokens, con
  *   expert_counts[nexperts]: each expert's slots.
  *   rows: the rows the buffers have room for, at least
  *     hc_expert_rows_bound(ntokens, k, nexperts, row_align).
+ * The calls that read a plan treat a row number outside [0, rows) as -1.
  * k in 1..HC_MAX_TOPK, nexperts in 1..HC_MAX_EXPERTS, row_align >= 1; slots
  * and rows < 2^31.
  */

@@ -505,6 +505,31 @@ def test_expert_rows(case, dtype):
         check_guards(wbuf, dweights)
 
 
+def test_row_numbers_outside_the_plan_count_as_none():
+    g = gen(25)
+    n, k, dim = 40, 3, 50
+    ids, plan = expert_case((n, k, 6, 4, dim, 6, 0), F, g)
+    x = torch.randn((n, dim), generator=g, device="cuda")
+    w = torch.rand((n, k), generator=g, device="cuda")
+    got = []
+    for none in (-1, plan.rows, (1 << 31) - 1, -(1 << 31)):
+        plan.row_of_slot[::5] = none
+        _, rows = guarded((plan.rows, dim), F)
+        buf, drows = guarded((plan.rows, dim), F)
+        out, dw = torch.empty_like(x), torch.empty_like(w)
+        hc.hc_expert_dispatch(x, plan, rows)
+        hc.hc_expert_combine(rows, plan, w, out)
+        hc.hc_expert_combine_grad(x, rows, plan, w, drows, dw)
+        got.append((rows.clone(), out, drows.clone(), dw))
+        check_guards(buf, drows)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    plan.expert_offsets[-1] = 1 << 30          # padding ends with the rows' room
+    buf, rows = guarded((plan.rows, dim), F)
+    hc.hc_expert_dispatch(x, plan, rows)
+    check_guards(buf, rows)
+
+
 def test_combine_gradients_against_differences():
     """<combine(rows, w), r>: its derivatives by every weight and by every row
     value, from differences of hc_expert_combine itself (it is linear in both)."""
