@@ -226,20 +226,25 @@ size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
 
 namespace {
 
-// Pieces that a launch of the sort zeroes beside it.
-constexpr uint64_t kPiecesBeside = 768;
+// Pieces that a launch of the sort zeroes beside it: 50 MB for one of a radix
+// sort's, 200 MB for the one that places all ids, which takes longer than the
+// others once there are thousands.  (The gradient of 32,768 x 2048 bf16 into
+// 100,003 fp32 rows with 12, 25, 50, 100 and 200 MB a launch: 208, 207, 203, 207
+// and 223 us; of 8000 x 2048 into 128,000 with 50, 100, 200 and 400 MB: 222, 217,
+// 207 and 207 us.)
+constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3072;
 
 hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws, ZeroJob* zero,
                     hipStream_t stream) {
   if (n == 0) return hipSuccess;
   uint32_t beside = 0;
-  auto next = [&]() {
+  auto next = [&](uint64_t most) {
     zero->done += beside;
-    beside = (uint32_t)(zero->pieces - zero->done < kPiecesBeside ? zero->pieces - zero->done : kPiecesBeside);
+    beside = (uint32_t)(zero->pieces - zero->done < most ? zero->pieces - zero->done : most);
   };
   if (by_rank(n, src.nkeys)) {
     const uint32_t groups = (uint32_t)((n + 63) / 64);
-    next();
+    next(kPiecesBesideRank);
     HC_ENQUEUE(rank_kernel, groups + beside, kSortThreads, stream, src, (uint32_t)n, keys, pos, groups, *zero);
     zero->done += beside;
     return hipSuccess;
@@ -257,9 +262,9 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
     p.bits = per;
     p.keys_out = last_buffer ? keys : tmp_keys;
     p.pos_out = last_buffer ? pos : tmp_pos;
-    next();
+    next(kPiecesBeside);
     HC_ENQUEUE(pass_histogram_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
-    next();
+    next(kPiecesBeside);
     HC_ENQUEUE(pass_scatter_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
     p.keys = p.keys_out;
     p.pos = p.pos_out;

@@ -262,6 +262,7 @@ GRADS = [
     (140_000, 600, 600, "falling", 0, torch.int32, None),
     # tables too large to be zeroed beside the sort; a sort whose tiles hold more than four items a lane
     (500, 40_000, 520, "falling", 0, torch.int64, None),
+    (700, 110_000, 500, "falling", 0, torch.int32, None),
     (5000, 150_000, 400, "outside", 0, torch.int64, None),
     (300_001, 5000, 9, "falling", 0, torch.int32, None),
     (400_003, 100, 10, "one", 0, torch.int32, None),
@@ -668,3 +669,22 @@ def test_calls_run_on_the_stream_they_are_given():
     side.synchronize()
     for o in OUTPUTS:
         assert torch.equal(s[o], want[o]), o
+
+
+def test_calls_on_a_stream_of_few_compute_units():
+    """No call waits for more workgroups than the stream's compute units hold."""
+    s, want = step_state(), step_state()
+    new_inputs(s, 60)
+    new_inputs(want, 60)
+    step_calls(want)
+    torch.cuda.synchronize()
+    handle = hc.hc_stream_create_cu_budget(8)
+    try:
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+            step_calls(s)
+        torch.cuda.synchronize()
+        for o in OUTPUTS:
+            assert torch.equal(s[o], want[o]), o
+    finally:
+        torch.cuda.synchronize()
+        hc.hc_stream_destroy(handle)
