@@ -523,6 +523,12 @@ def _dense(t: torch.Tensor) -> bool:
     return (_native or _load_native()).is_dense(t)
 
 
+def _norm_kind(norm: str) -> int:
+    if norm not in _NORMS:
+        raise ValueError(f"norm {norm!r} is none of {', '.join(_NORMS)}")
+    return _NORMS[norm]
+
+
 def hc_grad_norm_workspace_bytes(ntensors: int) -> int:
     return int(load().hc_grad_norm_workspace_bytes(ntensors))
 
@@ -530,7 +536,7 @@ def hc_grad_norm_workspace_bytes(ntensors: int) -> int:
 def hc_grad_norm(grads, d_norm: torch.Tensor, ws: torch.Tensor, *, norm: str = "l2", stream=None):
     """d_norm[0] = the norm of all grads as one vector ("l2" or "inf"); see
     include/hc.h.  Gradients may have any order of dimensions but no gaps."""
-    st = (_native or _load_native()).grad_norm(grads, d_norm, ws, _NORMS[norm], _raw_stream(stream))
+    st = (_native or _load_native()).grad_norm(grads, d_norm, ws, _norm_kind(norm), _raw_stream(stream))
     if st:
         _check(st)
 
@@ -547,7 +553,7 @@ def hc_clip_grad_norm(grads, max_norm: float, d_norm: torch.Tensor, ws: torch.Te
                       stream=None):
     """hc_grad_norm and hc_clip_grads in one call; d_norm[0] receives the norm
     before clipping."""
-    st = (_native or _load_native()).clip_grad_norm(grads, outs, _NORMS[norm], max_norm, d_norm, ws,
+    st = (_native or _load_native()).clip_grad_norm(grads, outs, _norm_kind(norm), max_norm, d_norm, ws,
                                                     _raw_stream(stream))
     if st:
         _check(st)

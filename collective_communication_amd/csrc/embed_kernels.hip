@@ -103,14 +103,15 @@ __device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
 
 // ---------------------------------------------------------------- sorting the ids
 
-// Ids up to this many are sorted in one launch: each workgroup places 64 ids,
-// its 16 waves comparing them with a sixteenth of all ids each.  n^2
-// comparisons, 2 instructions each, beat the launches of a radix sort while n
-// is small: up to 8192 where that takes two digits (the whole gradient of 8000
-// tokens x 256 bf16 into 5000 rows 24.0 us so, 27.3 by digits; of 10000, 27.7
-// and 27.8), up to 4096 where one digit does (into 500 rows, 6000 tokens 20.4
-// and 18.4).
+// Ids up to this many are sorted in one launch: a workgroup places kRankIds of
+// them, each of its waves comparing them with a sixteenth of all ids, a quarter
+// of that sixteenth per 16 lanes.  n^2 comparisons, 3 instructions each, spread
+// over all compute units, beat the launches of a radix sort while n is small.
+// The whole gradient of n x 256 bf16, us, so / by digits: into 20,000 rows (two
+// digits) 8000 tokens 22.7 / 28.3, 10,000 32.6 / 30.3; into 500 rows (one) 6000
+// tokens 19.4 / 18.7.  With 64 ids a workgroup 4096 tokens took 17.9, not 15.3.
 constexpr uint32_t kRankMax = 8192;
+constexpr uint32_t kRankIds = 16;
 inline bool by_rank(size_t n, size_t nkeys) { return n <= (nkeys <= kMaxRadix ? kRankMax / 2 : kRankMax); }
 
 __global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint32_t n, uint32_t* keys, uint32_t* pos,
@@ -120,38 +121,34 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(KeySource src, uint3
     return;
   }
   __shared__ __attribute__((aligned(16))) uint32_t all[kRankMax];
-  __shared__ uint32_t part[kSortWaves][64];
-  const uint32_t padded = (n + 63) & ~63u;
+  __shared__ uint32_t part[kSortWaves][kRankIds];
+  const uint32_t padded = (n + 255) & ~255u;
   for (uint32_t i = threadIdx.x; i < padded; i += kSortThreads) {
     const uint32_t k = i < n ? load_key(src, i) : kNoKey;
     all[i] = k < src.nkeys ? k : src.nkeys;     // no key sorts last
   }
   __syncthreads();
-  const uint32_t g0 = blockIdx.x * 64, i = g0 + lane_id();
+  const uint32_t g0 = blockIdx.x * kRankIds, i = g0 + lane_id() % kRankIds;
   const uint32_t key = all[i];
-  const uint32_t share = padded / kSortWaves;    // a multiple of 4
-  const uint32_t lo = wave_id() * share, hi = lo + share;
+  const uint32_t share = padded / (kSortWaves * 4);     // a multiple of 4
+  const uint32_t lo = (wave_id() * 4 + lane_id() / kRankIds) * share;
   uint32_t c = 0;
-  auto count4 = [&](uint32_t j, uint32_t below) {
-    const vec4 k = *reinterpret_cast<const vec4*>(&all[j]);
-    c += (k[0] < below) + (k[1] < below) + (k[2] < below) + (k[3] < below);
-  };
-  uint32_t j = lo;
 #pragma unroll 4
-  for (; j < hi && j < g0; j += 4) count4(j, key + 1);          // earlier ids: equal ones come first
-#pragma unroll 4
-  for (; j < hi && j < g0 + 64; j += 4) {
+  for (uint32_t j = lo; j < lo + share; j += 4) {
     const vec4 k = *reinterpret_cast<const vec4*>(&all[j]);
-#pragma unroll
-    for (uint32_t q = 0; q < 4; ++q) c += k[q] < key + (j + q < i ? 1 : 0);
+    const uint32_t below = key + (j < g0 ? 1 : 0);      // of earlier ids, equal ones come first too
+    const uint32_t four = (k[0] < below) + (k[1] < below) + (k[2] < below) + (k[3] < below);
+    c += j - g0 < kRankIds ? 0 : four;                  // the group's own: below
   }
-#pragma unroll 4
-  for (; j < hi; j += 4) count4(j, key);                        // later ids
-  part[threadIdx.x >> 6][lane_id()] = c;
+  c += __shfl_xor(c, 16);
+  c += __shfl_xor(c, 32);
+  if (lane_id() < kRankIds) part[threadIdx.x >> 6][lane_id()] = c;
   __syncthreads();
-  if (threadIdx.x < 64 && i < n) {
+  if (threadIdx.x < kRankIds && i < n) {
     uint32_t r = 0;
     for (uint32_t w = 0; w < kSortWaves; ++w) r += part[w][threadIdx.x];
+#pragma unroll
+    for (uint32_t q = 0; q < kRankIds; ++q) r += all[g0 + q] < key + (g0 + q < i ? 1 : 0);
     if (r < n) {
       keys[r] = key < src.nkeys ? key : kNoKey;
       pos[r] = i;
@@ -243,7 +240,7 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
     beside = (uint32_t)(zero->pieces - zero->done < most ? zero->pieces - zero->done : most);
   };
   if (by_rank(n, src.nkeys)) {
-    const uint32_t groups = (uint32_t)((n + 63) / 64);
+    const uint32_t groups = (uint32_t)((n + kRankIds - 1) / kRankIds);
     next(kPiecesBesideRank);
     HC_ENQUEUE(rank_kernel, groups + beside, kSortThreads, stream, src, (uint32_t)n, keys, pos, groups, *zero);
     zero->done += beside;

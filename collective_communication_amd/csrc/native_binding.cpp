@@ -145,9 +145,9 @@ Tensors tensors(const Sequence& s) {
   r.dtypes.reserve(n);
   for (size_t i = 0; i < n; ++i) {
     const at::Tensor& t = tensor(s[i], "a gradient");
+    r.dtypes.push_back(dtype_of(t));
     if (!t.is_cuda()) raise(PyExc_ValueError, "grads[%zu] is not a device tensor", i);
     if (!t.is_non_overlapping_and_dense()) raise(PyExc_ValueError, "grads[%zu] is not dense: its storage has gaps", i);
-    r.dtypes.push_back(dtype_of(t));
     r.p.push_back(t.data_ptr());
     r.counts.push_back((size_t)t.numel());
   }

@@ -192,6 +192,14 @@ def test_binding_refuses_host_tensors_and_wrong_types(hc):
         hc.hc_embedding(i, f, f.double())
     with pytest.raises(ValueError):
         hc.ExpertPlan.for_sizes(4, 2, 8, device="cpu")
+    with pytest.raises(ValueError, match="norm"):
+        hc.hc_grad_norm([], torch.zeros(1), torch.zeros(64), norm="l1")
+    with pytest.raises(TypeError):
+        hc.hc_grad_norm([f.double()], torch.zeros(1), torch.zeros(64))
+    with pytest.raises(TypeError):
+        hc.hc_grad_norm([1.0], torch.zeros(1), torch.zeros(64))
+    with pytest.raises(TypeError):
+        hc.hc_clip_grad_norm(7, 1.0, torch.zeros(1), torch.zeros(64))
 
 
 def test_dense_storage_rule(hc):
