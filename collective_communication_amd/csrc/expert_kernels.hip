@@ -11,8 +11,9 @@
 // one sum, so the side that is k times larger moves exactly once and the
 // other is not read k times over.  (By row instead, gathering each row's
 // token: 298 against 232 us for 16,384 x 8 rows of 4096 bf16.)  Sums run over j
-// in order within a lane: no atomics.  The token's row numbers are loaded once into the wave's lanes
-// and read from there as scalars, so every row's address is scalar.
+// in order within a lane: no atomics.  The token's row numbers are loaded once
+// into the wave's lanes and read from there as scalars, so every row's address
+// is scalar.
 #include <type_traits>
 
 #include "key_sort.hpp"
@@ -72,10 +73,20 @@ __global__ void __launch_bounds__(kSortThreads) expert_scatter_kernel(Sort s) {
     }
     if (e == 0) s.offsets[s.experts] = (int32_t)used;
   }
-  // rows without a slot: each expert's padding, spread over the tiles, and
-  // what lies behind the last expert
-  if (e < s.experts && e % gridDim.x == blockIdx.x)
-    for (uint32_t r = first + total; r < first + padded; ++r) s.slot_of_row[r] = -1;
+  // rows without a slot: each expert's padding, spread over the tiles (by the
+  // expert's lane, or by its wave where it may be long), and what lies behind
+  // the last expert
+  const bool mine = e < s.experts && e % gridDim.x == blockIdx.x;
+  if (s.align <= 64) {
+    if (mine)
+      for (uint32_t r = first + total; r < first + padded; ++r) s.slot_of_row[r] = -1;
+  } else {
+    for (uint64_t todo = __ballot(mine); todo; todo &= todo - 1) {
+      const uint32_t at = (uint32_t)__builtin_ctzll(todo);
+      const uint32_t end = lane_read(first + padded, at);
+      for (uint32_t r = lane_read(first + total, at) + lane_id(); r < end; r += 64) s.slot_of_row[r] = -1;
+    }
+  }
   for (size_t r = (size_t)used + blockIdx.x * kSortThreads + e; r < s.rows; r += (size_t)gridDim.x * kSortThreads)
     s.slot_of_row[r] = -1;
   place_items(counts, s.experts, s.bits, run, first + before, digit,

@@ -393,6 +393,7 @@ EXPERTS = [
     (33_000, 4, 129, 1, 24, 129, 0),
     (90_001, 4, 300, 3, 5, 300, 0),
     (50, 2, 4, 1000, 40, 4, 0),
+    (2100, 3, 70, 65, 9, 75, 2),
 ]
 
 
