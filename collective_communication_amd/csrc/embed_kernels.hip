@@ -229,7 +229,7 @@ namespace {
 // 100,003 fp32 rows with 12, 25, 50, 100 and 200 MB a launch: 208, 207, 203, 207
 // and 223 us; of 8000 x 2048 into 128,000 with 50, 100, 200 and 400 MB: 222, 217,
 // 207 and 207 us.)
-constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3072;
+constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3200;
 
 hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws, ZeroJob* zero,
                     hipStream_t stream) {
