@@ -85,24 +85,48 @@ struct Range {
   bool out;
 };
 
+// Whether the outputs, in their order, ascend without touching (the views of
+// one bucket do), with every gradient but an output's own outside their span:
+// then nothing overlaps, found without sorting.
+bool plainly_disjoint(const void* const* grads, void* const* outs, const size_t* counts, const hc_dtype_t* dtypes,
+                      size_t n) {
+  uintptr_t first = 0, end = 0;
+  for (size_t i = 0; i < n; ++i) {
+    if (!counts[i]) continue;
+    const uintptr_t o = (uintptr_t)outs[i];
+    if (o < end) return false;
+    if (!first) first = o;
+    end = o + counts[i] * esize(dtypes[i]);
+  }
+  for (size_t i = 0; i < n; ++i) {
+    const uintptr_t g = (uintptr_t)grads[i];
+    if (counts[i] && grads[i] != outs[i] && g < end && g + counts[i] * esize(dtypes[i]) > first) return false;
+  }
+  return true;
+}
+
 // Outputs must be disjoint from one another and from every gradient but their
-// own.  One sort by address: an output overlaps something when it begins
+// own.  Else one sort by address: an output overlaps something when it begins
 // before the furthest end so far, or when something begins before its end.
 hc_status_t check_outs(const void* const* grads, void* const* outs, const size_t* counts, const hc_dtype_t* dtypes,
                        size_t n) {
   if (!n) return HC_SUCCESS;
   if (!outs) return fail(HC_ERR_INVALID_ARGUMENT, "outs is NULL");
+  for (size_t i = 0; i < n; ++i) {
+    if (!counts[i]) continue;
+    if (!outs[i]) return fail(HC_ERR_INVALID_ARGUMENT, "outs[%zu] is NULL", i);
+    if ((uintptr_t)outs[i] % esize(dtypes[i]))
+      return fail(HC_ERR_INVALID_ARGUMENT, "outs[%zu] is not %zu-byte aligned", i, esize(dtypes[i]));
+  }
+  if (plainly_disjoint(grads, outs, counts, dtypes, n)) return HC_SUCCESS;
   std::vector<Range> r;
   r.reserve(2 * n);
   for (size_t i = 0; i < n; ++i) {
     if (!counts[i]) continue;
-    if (!outs[i]) return fail(HC_ERR_INVALID_ARGUMENT, "outs[%zu] is NULL", i);
-    const size_t es = esize(dtypes[i]);
-    if ((uintptr_t)outs[i] % es)
-      return fail(HC_ERR_INVALID_ARGUMENT, "outs[%zu] is not %zu-byte aligned", i, es);
+    const size_t bytes = counts[i] * esize(dtypes[i]);
     const uintptr_t o = (uintptr_t)outs[i], g = (uintptr_t)grads[i];
-    r.push_back({o, o + counts[i] * es, i, true});
-    if (o != g) r.push_back({g, g + counts[i] * es, i, false});
+    r.push_back({o, o + bytes, i, true});
+    if (o != g) r.push_back({g, g + bytes, i, false});
   }
   std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
   // the furthest ends of the outputs and of all ranges that began so far

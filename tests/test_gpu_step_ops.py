@@ -113,6 +113,41 @@ def test_norm_and_clip(name, types, kind):
         assert all(torch.equal(a, o) for a, o in zip(again, outs))
 
 
+@pytest.mark.parametrize("outs_flat", [True, False])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_views_of_buckets(gap, outs_flat):
+    """Views that follow one another in their buckets, fp32 and bf16 in turn,
+    some left out and (gap) some values between: as if they were apart."""
+    g = gen(6)
+    flat = {dt: torch.randn(400_000, generator=g, device="cuda").to(dt) for dt in (F, B)}
+    into = {dt: torch.full_like(flat[dt], GUARD) for dt in (F, B)}
+    at, xs, os, spots = {F: 0, B: 1}, [], [], []
+    for i in range(300):
+        dt, n = (F, B)[i * 7 % 3 % 2], (i * 131) % 1500
+        if i % 50 != 49:
+            xs.append(flat[dt][at[dt]:at[dt] + n])
+            os.append(into[dt][at[dt]:at[dt] + n] if outs_flat else torch.full((n,), GUARD, dtype=dt, device="cuda"))
+            spots.append((dt, at[dt], n))
+        at[dt] += n + gap
+    want = norm64(xs)
+    d = torch.zeros(1, device="cuda")
+    ws = space(hc.hc_grad_norm_workspace_bytes(len(xs)))
+    hc.hc_clip_grad_norm(xs, 1.0, d, ws, outs=os)
+    assert abs(float(d) - want) <= 1.01 * U * want
+    coef = min(1.0, 1.0 / (want + 1e-6))
+    for x, o in zip(xs, os):
+        w = x.double().cpu() * coef
+        close(o, w, w.abs() * (5.1 * U + HALF[x.dtype]) + TINY[x.dtype])
+    if outs_flat:
+        for dt, a, n in spots:
+            into[dt][a:a + n] = GUARD
+        assert all(bool((into[dt] == GUARD).all()) for dt in (F, B))
+    first = [o.clone() for o in os] if not outs_flat else None
+    hc.hc_clip_grad_norm(xs, 1.0, d, ws)              # in place
+    if first is not None:
+        assert all(torch.equal(x, o) for x, o in zip(xs, first))
+
+
 def test_clip_leaves_what_surrounds_it():
     g = gen(2)
     for dt in (F, B):
