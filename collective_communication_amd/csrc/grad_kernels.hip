@@ -37,6 +37,11 @@ constexpr uint32_t kBatch = 128;        // tensors per kernel argument: 3.6 KB o
 constexpr uint32_t kMaxGrid = 2048;     // 8 workgroups of 4 waves on each of 256 CUs
 constexpr uint32_t kMostBlocks = 1u << 23;   // of a launch: its lanes are counted in 32 bits
 constexpr uint32_t kStreamChunks = (uint32_t)(kStreamStoreBytes / kChunkBytes);
+// From here the norm reads non-temporal.  Plain reads leave the caches to the
+// clipping pass, until they only push each other out.  Both passes on bf16
+// values, plain / non-temporal, us: 134 MB 65.7 / 70.0, 268 MB 126 / 134,
+// 403 MB 193 / 198, 537 MB 265 / 263, 1.07 GB 549 / 531.
+constexpr uint32_t kStreamLoadChunks = (512u << 20) / kChunkBytes;
 // Up to here the clipping launch has at most kMaxGrid workgroups, which add the
 // partials up themselves; above it has one per chunk.
 constexpr uint32_t kFuseChunks = (128u << 20) / kChunkBytes;
@@ -243,7 +248,7 @@ __device__ __forceinline__ void norm_cut(const Place& p, double* acc, uint32_t& 
   }
 }
 
-template <bool INF>
+template <bool INF, bool NT>
 __device__ void norm_body(const Entry* e, const uint32_t* first, uint32_t n, uint32_t chunks, double* partials) {
   __shared__ double lds[kWaves];
   double acc[4] = {0, 0, 0, 0};
@@ -252,7 +257,7 @@ __device__ void norm_body(const Entry* e, const uint32_t* first, uint32_t n, uin
   Place p = place_of<false>(e, first, n, c);
   for (;;) {
     vec4 v[kVecs];
-    if (p.full) load_full<true>(p, v);
+    if (p.full) load_full<NT>(p, v);
     // the next chunk is looked up while this one's data are on their way
     c += gridDim.x;
     const bool more = c >= gridDim.x && c < chunks;
@@ -290,14 +295,14 @@ __device__ __forceinline__ float norm_of(const double* partials, uint32_t n) {
   return INF ? (float)v : (float)sqrt(v);
 }
 
-template <bool INF>
+template <bool INF, bool NT>
 __global__ void __launch_bounds__(kThreads) norm_args_kernel(Batch b, uint32_t n, uint32_t chunks, double* partials) {
-  norm_body<INF>(b.e, b.first, n, chunks, partials);
+  norm_body<INF, NT>(b.e, b.first, n, chunks, partials);
 }
-template <bool INF>
+template <bool INF, bool NT>
 __global__ void __launch_bounds__(kThreads) norm_table_kernel(TableView t, uint32_t n, uint32_t chunks,
                                                               double* partials) {
-  norm_body<INF>(t.e, t.first, n, chunks, partials);
+  norm_body<INF, NT>(t.e, t.first, n, chunks, partials);
 }
 
 template <bool INF>
@@ -506,11 +511,17 @@ hipError_t run_clip(const Plan& p, float max_norm, float* norm, const double* pa
 
 template <bool INF>
 hipError_t run(const Plan& p, bool clip, float max_norm, float* norm, double* partials, hipStream_t stream) {
-  if (p.grid) {
-    if (p.by_args)
-      HC_ENQUEUE(norm_args_kernel<INF>, p.grid, kThreads, stream, p.batch, p.n, p.chunks, partials);
+  const bool nt = p.chunks >= kStreamLoadChunks;
+  if (p.grid && p.by_args) {
+    if (nt)
+      HC_ENQUEUE((norm_args_kernel<INF, true>), p.grid, kThreads, stream, p.batch, p.n, p.chunks, partials);
     else
-      HC_ENQUEUE(norm_table_kernel<INF>, p.grid, kThreads, stream, p.view, p.n, p.chunks, partials);
+      HC_ENQUEUE((norm_args_kernel<INF, false>), p.grid, kThreads, stream, p.batch, p.n, p.chunks, partials);
+  } else if (p.grid) {
+    if (nt)
+      HC_ENQUEUE((norm_table_kernel<INF, true>), p.grid, kThreads, stream, p.view, p.n, p.chunks, partials);
+    else
+      HC_ENQUEUE((norm_table_kernel<INF, false>), p.grid, kThreads, stream, p.view, p.n, p.chunks, partials);
   }
   if (clip && p.grid && p.chunks <= kFuseChunks) return run_clip<INF>(p, max_norm, norm, partials, stream);
   HC_ENQUEUE(finish_kernel<INF>, 1, kThreads, stream, partials, p.grid, norm);

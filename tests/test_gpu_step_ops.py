@@ -223,6 +223,27 @@ def test_norm_of_more_than_2_to_32_values():
     assert int(x.count_nonzero()) == 3
 
 
+@pytest.mark.parametrize("kind", ["l2", "inf"])
+@pytest.mark.parametrize("apart", [3, 150])
+@pytest.mark.parametrize("values", [20_000_000, 90_000_000, 170_000_000])
+def test_norm_and_clip_of_large_buckets(values, apart, kind):
+    """fp32 and bf16 tensors, few and many, through the sizes where the passes
+    take other loads and stores; checked on the device, in slices of fp64."""
+    g = gen(7)
+    flat = torch.randn(values, generator=g, device="cuda")
+    n = values // apart
+    xs = [flat[i * n:i * n + n - 1 - i % 3].to((F, B)[i % 4 == 3]) for i in range(apart)]
+    parts = [(x.double().square().sum() if kind == "l2" else x.double().abs().max()) for x in xs]
+    total = torch.stack(parts)
+    want = float(total.sum().sqrt() if kind == "l2" else total.max())
+    norm, outs = clip(xs, 0.4 * want, norm=kind)
+    assert abs(norm - want) <= 1.01 * U * want
+    coef = 0.4 * want / (want + 1e-6)
+    for x, o in zip(xs, outs):
+        w = x.double() * coef
+        assert bool(((o.double() - w).abs() <= w.abs() * (5.1 * U + HALF[x.dtype]) + TINY[x.dtype]).all())
+
+
 # ------------------------------------------------------------------ embedding
 
 def make_ids(pattern, n, vocab, start, idt, g):
