@@ -16,8 +16,8 @@
 //
 // Measured: the lookup of 30,011 x 4096 bf16, a quarter of them in the table,
 // 40 us (246 MB written, 7.5 TB/s); the gradient of 32,768 x 2048 bf16 into
-// 100,003 fp32 rows 198-205 us, of which the sort 24 (45 with 200 MB zeroed
-// beside it): 1.0 GB in all, 0.85 of it written, 5.0 TB/s, as a large copy
+// 100,003 fp32 rows 194 us, of which the sort 24 (41 with 200 MB zeroed
+// beside it): 1.0 GB in all, 0.85 of it written, 5.2 TB/s, as a large copy
 // does.  Its parts alone: the sums 60-75 us, all the zeroing 117 us.
 #include "key_sort.hpp"
 #include "launch.hpp"
@@ -88,17 +88,26 @@ struct ZeroJob {
   uint64_t rows = 0, rows_per_piece = 0;
   uint64_t pieces = 0, done = 0;
   bool flat = false;
+  bool stream = false;                  // non-temporal
 };
 
+template <bool NT>
 __device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
   if (z.flat) {
     const uint64_t at = piece * kPieceBytes;
-    zero_span(z.base + at, z.row_bytes - at < kPieceBytes ? z.row_bytes - at : kPieceBytes, threadIdx.x, kSortThreads);
+    zero_span<NT>(z.base + at, z.row_bytes - at < kPieceBytes ? z.row_bytes - at : kPieceBytes, threadIdx.x,
+                  kSortThreads);
     return;
   }
   const uint64_t r0 = piece * z.rows_per_piece;
   for (uint64_t r = r0 + wave_id(); r < z.rows && r < r0 + z.rows_per_piece; r += kSortWaves)
-    zero_span(z.base + r * z.stride, z.row_bytes, lane_id(), 64);
+    zero_span<NT>(z.base + r * z.stride, z.row_bytes, lane_id(), 64);
+}
+__device__ __forceinline__ void zero_piece(const ZeroJob& z, uint64_t piece) {
+  if (z.stream)
+    zero_piece<true>(z, piece);
+  else
+    zero_piece<false>(z, piece);
 }
 
 // ---------------------------------------------------------------- sorting the ids
@@ -226,8 +235,8 @@ namespace {
 // Pieces that a launch of the sort zeroes beside it: 50 MB for one of a radix
 // sort's, 200 MB for the one that places all ids, which takes longer than the
 // others once there are thousands.  (The gradient of 32,768 x 2048 bf16 into
-// 100,003 fp32 rows with 12, 25, 50, 100 and 200 MB a launch: 208, 207, 203, 207
-// and 223 us; of 8000 x 2048 into 128,000 with 50, 100, 200 and 400 MB: 222, 217,
+// 100,003 fp32 rows with 25, 50, 75, 100 and 200 MB a launch: 202, 196, 196, 198
+// and 228 us; 16,000 tokens into 40,000 rows 92, 92, 100, 106, 113; of 8000 x 2048 into 128,000 with 50, 100, 200 and 400 MB: 222, 217,
 // 207 and 207 us.)
 constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3200;
 
@@ -295,6 +304,7 @@ struct Grad {
   uint32_t join_chunks;
   uint32_t zero_from;       // rows before it are zero already
   uint32_t zero_rows;       // table rows per zeroing workgroup
+  bool zero_stream;         // zeroed non-temporal
   uint64_t sum_units;
 };
 
@@ -408,7 +418,7 @@ __device__ __forceinline__ uint64_t rows_with_tokens(const Grad& g, uint32_t v0,
 
 // A workgroup zeroes those of its rows that no token has: a row at a time, or
 // several where a row is less than a wave's vectors.
-template <typename To>
+template <typename To, bool NT>
 __device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
   const uint32_t count = g.vocab - v0 < g.zero_rows ? g.vocab - v0 : g.zero_rows;
   const uint64_t all = count < 64 ? (1ull << count) - 1 : ~0ull;
@@ -419,13 +429,20 @@ __device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
     while (absent) {
       const uint32_t k = (uint32_t)__builtin_ctzll(absent);
       absent &= absent - 1;
-      zero_span(row(k), bytes, threadIdx.x, kThreads);
+      zero_span<NT>(row(k), bytes, threadIdx.x, kThreads);
     }
     return;
   }
   const uint32_t lanes = nvec == 1 ? 8 : 1u << (32 - __builtin_clz((uint32_t)nvec - 1));   // of a row
   for (uint32_t k = threadIdx.x / lanes; k < count; k += kThreads / lanes)
-    if (absent >> k & 1) zero_span(row(k), bytes, threadIdx.x % lanes, lanes);
+    if (absent >> k & 1) zero_span<NT>(row(k), bytes, threadIdx.x % lanes, lanes);
+}
+template <typename To>
+__device__ __forceinline__ void zero_rows(const Grad& g, uint32_t v0) {
+  if (g.zero_stream)
+    zero_rows<To, true>(g, v0);
+  else
+    zero_rows<To, false>(g, v0);
 }
 
 template <typename Ti, typename To, bool ACC>
@@ -610,7 +627,15 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   uint32_t* keys = reinterpret_cast<uint32_t*>(base + l.keys);
   uint32_t* pos = reinterpret_cast<uint32_t*>(base + l.pos);
   const size_t row_bytes = dim * (dwtype == HC_F32 ? 4 : 2), stride = wstride * (dwtype == HC_F32 ? 4 : 2);
+  // A large table's zeroes are stored non-temporal: plain ones push the tokens'
+  // rows out of the caches before they are summed.  Tokens x 2048 bf16 into
+  // rows of fp32, plain / non-temporal, us: 16,000 into 24,000 rows (197 MB) 81 /
+  // 75, into 40,000 102 / 92; 32,768 into 100,003 205 / 194; 2000 into 24,000 48 /
+  // 51, into 40,000 68 / 69.  Below, the table itself stays in the caches for
+  // its next reader.  (Sums stored non-temporal too: 201 where 194.)
+  const bool stream_zeroes = src.nkeys * row_bytes >= kStreamStoreBytes;
   ZeroJob zero;
+  zero.stream = stream_zeroes;
   if (!accumulate) {
     zero.base = static_cast<char*>(dweight);
     zero.flat = stride == row_bytes || src.nkeys == 1;
@@ -640,6 +665,7 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   const uint64_t zeroed = zero.done == zero.pieces ? src.nkeys
                           : zero.flat              ? zero.done * kPieceBytes / row_bytes
                                                    : zero.done * zero.rows_per_piece;
+  g.zero_stream = stream_zeroes;
   g.zero_from = accumulate ? g.vocab : (uint32_t)zeroed;
   g.zero_rows = row_bytes >= kZeroBytes / 4    ? 4
                 : row_bytes <= kZeroBytes / 64 ? 64

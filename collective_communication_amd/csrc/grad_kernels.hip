@@ -37,10 +37,12 @@ constexpr uint32_t kBatch = 128;        // tensors per kernel argument: 3.6 KB o
 constexpr uint32_t kMaxGrid = 2048;     // 8 workgroups of 4 waves on each of 256 CUs
 constexpr uint32_t kMostBlocks = 1u << 23;   // of a launch: its lanes are counted in 32 bits
 constexpr uint32_t kStreamChunks = (uint32_t)(kStreamStoreBytes / kChunkBytes);
-// From here the norm reads non-temporal.  Plain reads leave the caches to the
-// clipping pass, until they only push each other out.  Both passes on bf16
-// values, plain / non-temporal, us: 134 MB 65.7 / 70.0, 268 MB 126 / 134,
-// 403 MB 193 / 198, 537 MB 265 / 263, 1.07 GB 549 / 531.
+// The norm reads non-temporal, but for sizes whose clipping stores
+// non-temporal: that leaves the caches to the gradients, which plain reads keep
+// for it, until from here on they only push each other out.  Both passes on
+// bf16 values, plain / non-temporal, us: 67 MB 40.7 / 38.9, 101 MB 57.1 / 55.5,
+// 134 MB 65.7 / 70.0, 268 MB 126 / 134, 403 MB 193 / 198, 537 MB 265 / 263,
+// 1.07 GB 549 / 531.
 constexpr uint32_t kStreamLoadChunks = (512u << 20) / kChunkBytes;
 // Up to here the clipping launch has at most kMaxGrid workgroups, which add the
 // partials up themselves; above it has one per chunk.
@@ -511,7 +513,7 @@ hipError_t run_clip(const Plan& p, float max_norm, float* norm, const double* pa
 
 template <bool INF>
 hipError_t run(const Plan& p, bool clip, float max_norm, float* norm, double* partials, hipStream_t stream) {
-  const bool nt = p.chunks >= kStreamLoadChunks;
+  const bool nt = p.chunks < kStreamChunks || p.chunks >= kStreamLoadChunks;
   if (p.grid && p.by_args) {
     if (nt)
       HC_ENQUEUE((norm_args_kernel<INF, true>), p.grid, kThreads, stream, p.batch, p.n, p.chunks, partials);

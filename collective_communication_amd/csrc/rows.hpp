@@ -164,14 +164,16 @@ __device__ __forceinline__ void store_vals(typename To::raw* p, const float* f) 
   }
 }
 
-// A span of zeroes, `bytes` (a multiple of 2) from p on, by `lanes` lanes.
+// A span of zeroes, `bytes` (a multiple of 2) from p on, by `lanes` lanes;
+// NT: stored non-temporal.
+template <bool NT>
 __device__ __forceinline__ void zero_span(char* p, uint64_t bytes, uint32_t lane, uint32_t lanes) {
   if (bytes < 16) {
     if (lane < bytes / 2) reinterpret_cast<uint16_t*>(p)[lane] = 0;
     return;
   }
   for (uint64_t i = lane * 16; i < bytes; i += lanes * 16)
-    *reinterpret_cast<vec4_u*>(p + (i + 16 <= bytes ? i : bytes - 16)) = vec4{0, 0, 0, 0};
+    store_vec<F32, NT>(reinterpret_cast<uint32_t*>(p + (i + 16 <= bytes ? i : bytes - 16)), vec4{0, 0, 0, 0});
 }
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 63u; }
