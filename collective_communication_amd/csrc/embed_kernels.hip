@@ -236,8 +236,8 @@ namespace {
 // sort's, 200 MB for the one that places all ids, which takes longer than the
 // others once there are thousands.  (The gradient of 32,768 x 2048 bf16 into
 // 100,003 fp32 rows with 25, 50, 75, 100 and 200 MB a launch: 202, 196, 196, 198
-// and 228 us; 16,000 tokens into 40,000 rows 92, 92, 100, 106, 113; of 8000 x 2048 into 128,000 with 50, 100, 200 and 400 MB: 222, 217,
-// 207 and 207 us.)
+// and 228 us; of 16,000 into 40,000 rows 92, 92, 100, 106 and 113; of 8000 x 2048
+// into 128,000, one launch, with 50, 100, 200 and 400 MB: 222, 217, 207 and 207.)
 constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3200;
 
 hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws, ZeroJob* zero,
