@@ -232,25 +232,24 @@ size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
 
 namespace {
 
-// Pieces that a launch of the sort zeroes beside it: 50 MB for one of a radix
-// sort's, 200 MB for the one that places all ids, which takes longer than the
-// others once there are thousands.  (The gradient of 32,768 x 2048 bf16 into
-// 100,003 fp32 rows with 25, 50, 75, 100 and 200 MB a launch: 202, 196, 196, 198
-// and 228 us; of 16,000 into 40,000 rows 92, 92, 100, 106 and 113; of 8000 x 2048
-// into 128,000, one launch, with 50, 100, 200 and 400 MB: 222, 217, 207 and 207.)
-constexpr uint64_t kPiecesBeside = 768, kPiecesBesideRank = 3200;
+// Pieces that a launch of the sort zeroes beside it, 50 MB.  The gradient with
+// 25, 50, 100 and 200 MB a launch, us: 32,768 x 2048 bf16 into 100,003 fp32 rows
+// 202, 196, 198 and 228; 16,000 into 40,000 rows 92, 92, 106 and 113; placed by one
+// launch, 8000 into 128,000 rows 210, 210, 212 and 213, 500 into 30,000 47, 47, 49
+// and 54, 2000 into 40,000 65, 63, 65 and 68.
+constexpr uint64_t kPiecesBeside = 768;
 
 hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* pos, void* ws, ZeroJob* zero,
                     hipStream_t stream) {
   if (n == 0) return hipSuccess;
   uint32_t beside = 0;
-  auto next = [&](uint64_t most) {
+  auto next = [&] {
     zero->done += beside;
-    beside = (uint32_t)(zero->pieces - zero->done < most ? zero->pieces - zero->done : most);
+    beside = (uint32_t)(zero->pieces - zero->done < kPiecesBeside ? zero->pieces - zero->done : kPiecesBeside);
   };
   if (by_rank(n, src.nkeys)) {
     const uint32_t groups = (uint32_t)((n + kRankIds - 1) / kRankIds);
-    next(kPiecesBesideRank);
+    next();
     HC_ENQUEUE(rank_kernel, groups + beside, kSortThreads, stream, src, (uint32_t)n, keys, pos, groups, *zero);
     zero->done += beside;
     return hipSuccess;
@@ -268,9 +267,9 @@ hipError_t sort_ids(const KeySource& src, size_t n, uint32_t* keys, uint32_t* po
     p.bits = per;
     p.keys_out = last_buffer ? keys : tmp_keys;
     p.pos_out = last_buffer ? pos : tmp_pos;
-    next(kPiecesBeside);
+    next();
     HC_ENQUEUE(pass_histogram_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
-    next(kPiecesBeside);
+    next();
     HC_ENQUEUE(pass_scatter_kernel, p.tiles + beside, kSortThreads, stream, p, *zero);
     p.keys = p.keys_out;
     p.pos = p.pos_out;
