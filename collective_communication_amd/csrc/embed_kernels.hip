@@ -628,10 +628,11 @@ hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const voi
   const size_t row_bytes = dim * (dwtype == HC_F32 ? 4 : 2), stride = wstride * (dwtype == HC_F32 ? 4 : 2);
   // A large table's zeroes are stored non-temporal: plain ones push the tokens'
   // rows out of the caches before they are summed.  Tokens x 2048 bf16 into
-  // rows of fp32, plain / non-temporal, us: 16,000 into 24,000 rows (197 MB) 81 /
-  // 75, into 40,000 102 / 92; 32,768 into 100,003 205 / 194; 2000 into 24,000 48 /
-  // 51, into 40,000 68 / 69.  Below, the table itself stays in the caches for
-  // its next reader.  (Sums stored non-temporal too: 201 where 194.)
+  // rows of fp32, plain / non-temporal, us: 2000 into 24,000 rows (197 MB) 45 / 41,
+  // into 40,000 68 / 63; 16,000 into 24,000 81 / 75, into 40,000 102 / 91; 32,768
+  // into 100,003 205 / 194.  Below, the gain is small (2000 into 12,000 28 / 26), and
+  // the table itself stays in the caches for its next reader.  (Sums stored
+  // non-temporal too: 201 where 194.)
   const bool stream_zeroes = src.nkeys * row_bytes >= kStreamStoreBytes;
   ZeroJob zero;
   zero.stream = stream_zeroes;
