@@ -340,7 +340,9 @@ Rows rows_of(const hc_expert_plan_t& plan, size_t dim) {
 }  // namespace
 
 size_t expert_sort_ws_bytes(size_t nslots, size_t nexperts) {
-  return nslots <= kSelfCount ? 0 : sort_tiles(nslots) * nexperts * sizeof(uint32_t);
+  // as if for kMaxTiles tiles: their number falls where a tile grows (64 at
+  // 65,536 slots, 33 at 65,537), and a workspace has to do for fewer slots too
+  return nslots <= kSelfCount ? 0 : (size_t)kMaxTiles * nexperts * sizeof(uint32_t);
 }
 
 hipError_t launch_expert_sort(const KeySource& src, const hc_expert_plan_t& plan, void* ws, hipStream_t stream) {

@@ -653,6 +653,8 @@ typedef struct {
 
 /* ntokens * k + min(nexperts, ntokens * k) * (row_align - 1); 0 on invalid sizes. */
 size_t hc_expert_rows_bound(size_t ntokens, int k, int nexperts, int row_align);
+/* 0 where no workspace is needed, and on invalid sizes.  Enough for fewer slots
+ * and experts as well. */
 size_t hc_expert_sort_workspace_bytes(size_t nslots, int nexperts);
 /* experts: ntokens * k device integers of id_bytes (4 or 8) bytes; this
  * rank's experts are [expert_start, expert_start + nexperts). */

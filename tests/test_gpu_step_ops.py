@@ -492,6 +492,19 @@ def test_expert_sort(case, idt):
         assert a.tolist() == b, name
 
 
+def test_one_sort_workspace_for_all_batches():
+    """The workspace of the largest batch serves the smaller ones."""
+    g = gen(26)
+    k, e = 2, 128
+    ws = space(hc.hc_expert_sort_workspace_bytes(35_000 * k, e))
+    for n in (35_000, 32_768, 30_000, 2500, 7):
+        ids = torch.randint(0, e, (n, k), generator=g, device="cuda")
+        plan = hc.ExpertPlan.for_sizes(n, k, e)
+        hc.hc_expert_sort(ids, plan, ws)
+        want = torch.sort(ids.reshape(-1), stable=True).indices.int()
+        assert torch.equal(plan.slot_of_row, want), n
+
+
 @pytest.mark.parametrize("tokens", [700, 40_000])
 def test_expert_sort_when_all_choose_one(tokens):
     for chosen in (0, 4):                 # an expert of ours, then none of ours

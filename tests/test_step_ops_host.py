@@ -54,6 +54,22 @@ def test_workspaces_grow_and_cover(hc):
     assert 0 < a < b and b >= 2 * 4 * 100_000                        # keys and places of every token
 
 
+def test_expert_sort_workspaces_serve_fewer_slots_and_experts(hc):
+    """A workspace for some sizes is enough for all that are none larger."""
+    slots = sorted({max(0, n + d) for n in (0, 1, 1000, 4096, 10_000, 60_000, 65_536, 70_000, 131_072, 1 << 20,
+                                            (1 << 31) - 2) for d in (-1, 0, 1)})
+    for e in (1, 3, 128, 1023, 1024):
+        size = [hc.hc_expert_sort_workspace_bytes(n, e) for n in slots]
+        assert size == sorted(size), [(n, s) for n, s in zip(slots, size)]
+        assert all(hc.hc_expert_sort_workspace_bytes(n, max(1, e - 1)) <= s for n, s in zip(slots, size))
+    # the call itself: past the check of the size, the misaligned workspace is what it refuses
+    L, room = hc.load(), hc.hc_expert_sort_workspace_bytes(70_000, 128)
+    for n in (70_000, 65_536, 60_000, 33_000, 5000):
+        plan = plan_of(hc, ntokens=n, k=1, nexperts=128, row_align=1, rows=n)
+        assert L.hc_expert_sort(Q, 4, 0, ctypes.byref(plan), W + 8, room, None) == hc.HC_ERR_INVALID_ARGUMENT
+        assert b"aligned" in L.hc_last_error(), (n, L.hc_last_error())
+
+
 # ------------------------------------------------------------------ gradients
 
 def test_norm_refusals(hc):
