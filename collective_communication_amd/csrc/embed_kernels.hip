@@ -226,8 +226,9 @@ __global__ void __launch_bounds__(kSortThreads) pass_scatter_kernel(Pass p, Zero
 
 constexpr size_t kHistBytes = (size_t)kMaxTiles * kMaxRadix * sizeof(uint32_t);
 
-size_t sort_ids_ws_bytes(size_t n, size_t nkeys) {
-  return by_rank(n, nkeys) ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
+// Of any number of keys: fewer of them may take a longer sort.
+size_t sort_ids_ws_bytes(size_t n) {
+  return by_rank(n, 1) ? 0 : kHistBytes + (2 * n * sizeof(uint32_t) + 15) / 16 * 16;
 }
 
 namespace {
@@ -539,26 +540,46 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Grad g, uint32_t join_bl
 // otherwise, long ones where they do, for fewer partials (the gradient of
 // 60000 tokens x 4096 bf16, 32 and 64 tokens a chunk: 224 and 215 us; of 32000,
 // 155 and 151; of 32768 x 2048, 205 and 207).
+struct ChunkStep {
+  uint32_t tokens;
+  size_t work;      // from here on: tokens times slices of 256 columns
+};
+constexpr ChunkStep kChunkSteps[] = {{64, 4096 * 96}, {32, 4096 * 32}, {16, 4096 * 16}, {8, 0}};
 uint32_t chunk_tokens(size_t n, size_t dim) {
   const size_t work = n * ((dim + 255) / 256);
-  if (work >= (size_t)4096 * 96) return 64;
-  if (work >= (size_t)4096 * 32) return 32;
-  if (work >= (size_t)4096 * 16) return 16;
+  for (const ChunkStep& s : kChunkSteps)
+    if (work >= s.work) return s.tokens;
   return 8;
+}
+
+// Values of the partials, at least, for every batch of up to n tokens and
+// columns: not this batch's own, which are half as many wherever a chunk grows.
+// A batch of n' tokens x w columns (w a multiple of 4) in chunks of c needs
+// 2 * ceil(n' / c) * w <= 2 * (n' * w / c + w), and n' * w stays below 256
+// times the work from which on chunks are longer.
+size_t partial_values(size_t n, size_t dim) {
+  const size_t width = (dim + 3) / 4 * 4;
+  size_t most = 0, below = SIZE_MAX;
+  for (const ChunkStep& s : kChunkSteps) {
+    const size_t values = n * width < below ? n * width : below;
+    const size_t v = (values + s.tokens - 1) / s.tokens;
+    if (v > most) most = v;
+    below = s.work * 256;
+  }
+  return n ? 2 * (most + width) : 0;
 }
 
 struct GradLayout {
   size_t keys, pos, sort, partial, bytes;
 };
-GradLayout grad_layout(size_t n, size_t vocab, size_t dim) {
+GradLayout grad_layout(size_t n, size_t dim) {
   auto up = [](size_t x) { return (x + 15) & ~(size_t)15; };
-  const uint32_t chunk = chunk_tokens(n, dim);
   GradLayout l;
   l.keys = 0;
   l.pos = up(n * 4);
   l.sort = l.pos + up(n * 4);
-  l.partial = l.sort + up(sort_ids_ws_bytes(n, vocab));
-  l.bytes = l.partial + (n + chunk - 1) / chunk * 2 * ((dim + 3) / 4 * 4) * sizeof(float);
+  l.partial = l.sort + up(sort_ids_ws_bytes(n));
+  l.bytes = l.partial + partial_values(n, dim) * sizeof(float);
   return l;
 }
 
@@ -614,14 +635,12 @@ hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* we
   return dim < BF16::kVec ? run(BF16S{}) : run(BF16{});
 }
 
-size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim) {
-  return grad_layout(ntokens, vocab, dim).bytes;
-}
+size_t embedding_grad_ws_bytes(size_t ntokens, size_t dim) { return grad_layout(ntokens, dim).bytes; }
 
 hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const void* dout, hc_dtype_t dtype, size_t dim,
                                  size_t dstride, float scale, void* dweight, hc_dtype_t dwtype, size_t wstride,
                                  bool accumulate, void* ws, hipStream_t stream) {
-  const GradLayout l = grad_layout(ntokens, src.nkeys, dim);
+  const GradLayout l = grad_layout(ntokens, dim);
   char* base = static_cast<char*>(ws);
   uint32_t* keys = reinterpret_cast<uint32_t*>(base + l.keys);
   uint32_t* pos = reinterpret_cast<uint32_t*>(base + l.pos);

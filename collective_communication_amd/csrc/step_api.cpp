@@ -266,7 +266,7 @@ hc_status_t hc_embedding(const void* ids, int id_bytes, size_t ntokens, const vo
 
 size_t hc_embedding_grad_workspace_bytes(size_t ntokens, size_t vocab, size_t dim) {
   if (ntokens > kMax31 || vocab > kMax31 || dim > kMax31) return 0;
-  return hc::embedding_grad_ws_bytes(ntokens, vocab, dim);
+  return hc::embedding_grad_ws_bytes(ntokens, dim);
 }
 
 hc_status_t hc_embedding_grad(const void* ids, int id_bytes, size_t ntokens, const void* dout, hc_dtype_t dout_dtype,
@@ -280,7 +280,7 @@ hc_status_t hc_embedding_grad(const void* ids, int id_bytes, size_t ntokens, con
   HC_TRY(check_ids(ids, id_bytes, ntokens, "ids"));
   HC_TRY(check_rows(dout, dout_dtype, ntokens, dim, dout_stride, "dout"));
   HC_TRY(check_rows(dweight, dweight_dtype, vocab, dim, dweight_stride, "dweight"));
-  HC_TRY(check_ws(ws, ws_bytes, hc::embedding_grad_ws_bytes(ntokens, vocab, dim)));
+  HC_TRY(check_ws(ws, ws_bytes, hc::embedding_grad_ws_bytes(ntokens, dim)));
   if (hc::log_enabled())
     hc::log_line("hc_embedding_grad: tokens=%zu vocab=%zu dim=%zu dtypes=%s,%s accumulate=%d", ntokens, vocab, dim,
                  dout_dtype == HC_F32 ? "f32" : "bf16", dweight_dtype == HC_F32 ? "f32" : "bf16", accumulate != 0);

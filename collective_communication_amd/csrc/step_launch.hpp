@@ -58,7 +58,7 @@ constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 // ---- embedding (embed_kernels.hip)
 hipError_t launch_embedding(const KeySource& src, size_t ntokens, const void* weight, hc_dtype_t dtype, size_t dim,
                             size_t wstride, float scale, void* out, size_t ostride, hipStream_t stream);
-size_t embedding_grad_ws_bytes(size_t ntokens, size_t vocab, size_t dim);
+size_t embedding_grad_ws_bytes(size_t ntokens, size_t dim);   // of any number of table rows
 hipError_t launch_embedding_grad(const KeySource& src, size_t ntokens, const void* dout, hc_dtype_t dtype, size_t dim,
                                  size_t dstride, float scale, void* dweight, hc_dtype_t dwtype, size_t wstride,
                                  bool accumulate, void* ws, hipStream_t stream);

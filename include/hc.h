@@ -606,7 +606,8 @@ hc_status_t hc_embedding(const void *ids, int id_bytes, size_t ntokens, const vo
  *     nothing; a negative value names none.
  *   dout: ntokens rows of dout_dtype, dout_stride apart; dweight: vocab rows
  *     of dweight_dtype, dweight_stride apart.
- *   ws: hc_embedding_grad_workspace_bytes(ntokens, vocab, dim) bytes.
+ *   ws: hc_embedding_grad_workspace_bytes(ntokens, vocab, dim) bytes, which are
+ *     enough for fewer tokens, rows and columns as well (0 on invalid sizes).
  */
 size_t hc_embedding_grad_workspace_bytes(size_t ntokens, size_t vocab, size_t dim);
 hc_status_t hc_embedding_grad(const void *ids, int id_bytes, size_t ntokens, const void *dout,

@@ -369,6 +369,26 @@ def test_embedding_grad(case, types):
         check_guards(buf, dw)
 
 
+def test_one_gradient_workspace_for_all_batches():
+    """The workspace of the largest batch serves smaller ones, narrower tables
+    and fewer rows, and only the sizes asked for are needed."""
+    g = gen(16)
+    ws = space(hc.hc_embedding_grad_workspace_bytes(16_500, 3000, 1024))
+    for n, vocab, dim in ((16_500, 3000, 1024), (16_300, 3000, 1024), (8192, 3000, 1024), (8191, 1000, 1024),
+                          (5000, 1000, 1024), (16_500, 3000, 255), (3, 1, 1)):
+        ids = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+        dout = torch.randint(-4, 5, (n, dim), generator=g, device="cuda").float()     # sums are exact
+        want = torch.zeros((vocab, dim), dtype=torch.float64).index_add_(0, ids.cpu(), dout.cpu().double())
+        room = hc.hc_embedding_grad_workspace_bytes(n, vocab, dim)
+        assert room <= ws.numel()
+        own = torch.full((room + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        for w in (ws, own[:room]):
+            dw = torch.full((vocab, dim), GUARD, device="cuda")
+            hc.hc_embedding_grad(ids, dout, dw, w)
+            assert torch.equal(dw.double().cpu(), want), (n, vocab, dim)
+        assert bool((own[room:] == 0xA5).all()), "written past the workspace"
+
+
 def test_embedding_grad_against_differences():
     """d/dW of <out, r> by differences of the lookup's own output (fp32; the
     lookup is linear, so a step of 1 is exact up to rounding)."""

@@ -70,6 +70,40 @@ def test_expert_sort_workspaces_serve_fewer_slots_and_experts(hc):
         assert b"aligned" in L.hc_last_error(), (n, L.hc_last_error())
 
 
+def test_embedding_grad_workspaces_serve_smaller_batches(hc):
+    """The same for the gradient of a table: fewer tokens, rows or columns."""
+    f = hc.hc_embedding_grad_workspace_bytes
+    near = lambda *v: sorted({max(0, x + d) for x in v for d in (-1, 0, 1)})  # noqa: E731
+    tokens = near(0, 7, 64, 1000, 4096, 8192, 16_384, 20_000, 24_576, 32_768, 65_536, 98_304, 393_216, 1 << 20,
+                  (1 << 31) - 2)
+    rows = near(1, 500, 1024, 100_003, (1 << 31) - 2)
+    columns = near(1, 8, 255, 256, 512, 1024, 2048, 4096, 8192, 1 << 20, (1 << 31) - 2)
+    for v in rows:
+        for d in columns:
+            size = [f(n, v, d) for n in tokens]
+            assert size == sorted(size), (v, d)
+    for n in tokens:
+        for d in columns:
+            size = [f(n, v, d) for v in rows]
+            assert size == sorted(size), (n, d)
+        for v in rows:
+            size = [f(n, v, d) for d in columns]
+            assert size == sorted(size), (n, v)
+    # what the call lays out: keys and places, the long sort's histograms and pairs, two partials per chunk
+    for n, v, d, chunk, scratch in ((8191, 100_003, 4096, 16, 0), (8192, 100_003, 4096, 32, 0), (100, 10, 300, 8, 0),
+                                    (24_575, 100_003, 4096, 32, 1), (32_768, 100_003, 4096, 64, 1),
+                                    (5000, 1024, 64, 8, 1)):
+        need = 8 * n + scratch * (64 * 1024 * 4 + 8 * n) + -(-n // chunk) * 2 * 4 * d
+        assert f(n, v, d) >= need, (n, v, d)
+    # the call itself: past the check of the size, the misaligned workspace is what it refuses
+    L, room = hc.load(), f(32_768, 100_003, 4096)
+    for n, v, d in ((32_768, 100_003, 4096), (24_575, 100_003, 4096), (8191, 100_003, 4096), (8000, 1000, 4096),
+                    (32_768, 100_003, 511), (1, 1, 1)):
+        assert L.hc_embedding_grad(P, 4, n, Q, 1, d, v, d, 0, -1, 1.0, W, 0, d, 0, W + 8, room,
+                                   None) == hc.HC_ERR_INVALID_ARGUMENT
+        assert b"aligned" in L.hc_last_error(), (n, v, d, L.hc_last_error())
+
+
 # ------------------------------------------------------------------ gradients
 
 def test_norm_refusals(hc):
