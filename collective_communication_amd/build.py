@@ -4,17 +4,25 @@ Flags: -O3, -ffp-contract=off (no fused multiply-add contraction: every hop is
 one IEEE add), no fast-math, no flush-to-zero, packed-fp32 instructions
 disabled on the device (-Xclang -target-feature -Xclang -packed-fp32-ops).
 Objects go to _build/ at the repository root; the library lands next to this
-file so that it travels with the tree, and so does _native.so, the module that
-marshals torch tensors to it for calls where Python's share would be the larger.  The two measurement programs of
+file so that it travels with the tree.  The two measurement programs of
 measure/ at the repository root are built there: dma_contention (linked
 against libhc and rocBLAS from the system ROCm) and hbm_ceiling.
+
+Beside the library lands _native.so, the module that marshals torch tensors to
+it for calls where Python's share would be the larger.  It needs torch, its and
+Python's headers and a host compiler, which the library and the programs do
+not: they are built whatever becomes of it, and where one of these is missing
+it is left out with a message (the binding's calls that go through it then
+raise ImportError).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -48,10 +56,22 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _native_lacks() -> str | None:
+    """What _native.so needs that is not here, or None."""
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    for path in (os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                              "python_variable.h"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return path
+    return None if shutil.which(CXX) else f"the compiler {CXX}"
+
+
 def _compile_native() -> str:
     """native_binding.cpp, host code against torch's and Python's headers."""
-    import sysconfig
-
     import torch
 
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -81,20 +101,8 @@ def _link_native(obj: str):
     os.replace(tmp, NATIVE)
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(SOURCES) + 1, max(1, min(8, os.cpu_count() or 1)))
-    with cf.ThreadPoolExecutor(jobs) as ex:
-        native = ex.submit(_compile_native)
-        objs = list(ex.map(_compile, SOURCES))
-        native_obj = native.result()
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_native(native_obj)
+def _build_tools():
+    """The measurement programs."""
     tmp = DMA_TOOL + ".tmp"
     cmd = [HIPCC, *COMMON, *DEVICE, "-x", "hip", os.path.join(MEASURE, "dma_contention.hip"), "-o", tmp,
            "-L", PKG, "-lhc", "-Wl,-rpath,$ORIGIN/../collective_communication_amd", "-L/opt/rocm/lib", "-lrocblas", "-Wl,-rpath,/opt/rocm/lib"]
@@ -108,8 +116,34 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"hbm_ceiling build failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CEILING_TOOL)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    lacks = _native_lacks()
+    jobs = min(len(SOURCES) + 1, max(1, min(8, os.cpu_count() or 1)))
+    with cf.ThreadPoolExecutor(jobs) as ex:
+        native = None if lacks else ex.submit(_compile_native)
+        objs = list(ex.map(_compile, SOURCES))
+    tmp = LIB + ".tmp"
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LIB)
+    done = False
+    try:
+        if native:
+            _link_native(native.result())
+            done = True
+        else:
+            print(f"_native.so is not built: {lacks} is missing", file=sys.stderr)
+    finally:
+        if not done and os.path.exists(NATIVE):
+            os.remove(NATIVE)     # of the library that was here before
+        _build_tools()
     if verbose:
-        print(f"built {LIB}, {NATIVE}, {DMA_TOOL} and {CEILING_TOOL}")
+        print("built " + ", ".join(p for p in (LIB, None if lacks else NATIVE, DMA_TOOL, CEILING_TOOL) if p))
     return LIB
 
 

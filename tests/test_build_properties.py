@@ -82,3 +82,46 @@ def test_register_budgets_of_the_codec_kernels():
     assert len(one_block) >= 6, list(codec)
     for n, v in one_block.items():
         assert v["VGPRs"] <= 64 and v["ScratchSize [bytes/lane]"] == 0, (n, v)
+
+
+@pytest.fixture
+def small_build(monkeypatch, tmp_path):
+    """The build, of one host source and without the measurement programs, into a folder of its own."""
+    from collective_communication_amd import build as b
+
+    for name, value in (("SOURCES", ["schedule.cpp"]), ("BUILD", str(tmp_path / "obj")),
+                        ("LIB", str(tmp_path / "libhc.so")), ("NATIVE", str(tmp_path / "_native.so")),
+                        ("_build_tools", lambda: None)):
+        monkeypatch.setattr(b, name, value, raising=False)
+    with open(b.NATIVE, "w") as f:
+        f.write("of an older library")
+    return b
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not installed")
+@pytest.mark.parametrize("lacking", ["torch", "its headers", "the compiler"])
+def test_the_library_is_built_without_what_only_the_torch_module_needs(small_build, monkeypatch, capfd, lacking):
+    import sys
+
+    import torch
+
+    if lacking == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    elif lacking == "its headers":
+        monkeypatch.setattr(torch, "__file__", "/nonexistent/torch/__init__.py")
+    else:
+        monkeypatch.setattr(small_build, "CXX", "/nonexistent/g++")
+    assert small_build.build() == small_build.LIB and os.path.exists(small_build.LIB)
+    assert not os.path.exists(small_build.NATIVE), "a module of an older library stays beside the new one"
+    assert "_native.so is not built" in capfd.readouterr().err
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not installed")
+def test_a_module_that_does_not_compile_is_an_error_after_the_library(small_build, monkeypatch, tmp_path):
+    compiler = tmp_path / "broken"
+    compiler.write_text("#!/bin/sh\nexit 1\n")
+    compiler.chmod(0o755)
+    monkeypatch.setattr(small_build, "CXX", str(compiler))
+    with pytest.raises(RuntimeError, match="native_binding"):
+        small_build.build()
+    assert os.path.exists(small_build.LIB)
