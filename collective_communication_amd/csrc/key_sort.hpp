@@ -35,9 +35,10 @@ inline uint32_t sort_tiles(size_t n) { return (uint32_t)((n + sort_tile(n) - 1) 
 __device__ __forceinline__ uint32_t load_key(const KeySource& s, size_t i) {
   const int64_t id =
       s.id_bytes == 8 ? static_cast<const int64_t*>(s.ids)[i] : (int64_t)static_cast<const int32_t*>(s.ids)[i];
-  // unsigned wrap-around: an id below start becomes a huge difference
+  // the unsigned difference is exact for an id from start on; below it, it would
+  // pass for a key where start + nkeys is past the ids' type
   const uint64_t k = (uint64_t)id - (uint64_t)s.start;
-  if (k >= s.nkeys || (s.use_skip && id == s.skip)) return kNoKey;
+  if (id < s.start || k >= s.nkeys || (s.use_skip && id == s.skip)) return kNoKey;
   return (uint32_t)k;
 }
 

@@ -674,6 +674,28 @@ def test_expert_offsets_past_2_to_32():
     assert torch.equal(rows, small)
 
 
+@pytest.mark.parametrize("start", [(1 << 63) - 3, -(1 << 63)])
+def test_ids_at_the_ends_of_64_bits(start):
+    """A range that begins near an end of the ids' type holds the ids from its
+    start on, and none from the other end."""
+    top, low, vocab, dim = (1 << 63) - 1, -(1 << 63), 10, 12
+    ids = torch.tensor([low, low + 1, low + 6, top - 7, top - 2, top - 1, top, 0], device="cuda")
+    keys = [i - start if start <= i < start + vocab else -1 for i in ids.tolist()]
+    weight = torch.randn((vocab, dim), generator=gen(27), device="cuda")
+    out, dw = torch.full((len(keys), dim), GUARD, device="cuda"), torch.full((vocab, dim), GUARD, device="cuda")
+    hc.hc_embedding(ids, weight, out, vocab_start=start)
+    want = torch.stack([weight[k] if k >= 0 else torch.zeros(dim, device="cuda") for k in keys])
+    assert torch.equal(out, want), keys
+    dout = torch.arange(1.0, len(keys) + 1, device="cuda")[:, None].expand(-1, dim).contiguous()
+    hc.hc_embedding_grad(ids, dout, dw, space(hc.hc_embedding_grad_workspace_bytes(len(keys), vocab, dim)),
+                         vocab_start=start)
+    sums = [sum(t + 1.0 for t, k in enumerate(keys) if k == v) for v in range(vocab)]
+    assert dw[:, 0].tolist() == sums, keys
+    plan = hc.ExpertPlan.for_sizes(len(keys), 1, vocab)
+    hc.hc_expert_sort(ids, plan, expert_start=start)
+    assert plan.expert_counts.tolist() == [keys.count(v) for v in range(vocab)], keys
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def step_calls(s):
