@@ -535,12 +535,13 @@ int hc_copy_engine_available(void);
  * the ranks sum, and what happens to the sum before the update.
  *
  * All of these are asynchronous on `stream`, may be captured into a graph,
- * and give the same bits on every run: every sum has a fixed order.  Elements
- * are fp32 or bf16; bf16 is widened exactly, sums are held in fp32 (the norm
- * in fp64) and each result is rounded once, to nearest even.  Pointers need
- * only their element's alignment, except workspaces (16 bytes); rows may be
- * further apart than they are wide (strides in elements, never less than the
- * width).  Offsets are 64-bit.  Outputs must not overlap inputs unless a call
+ * and give the same bits when they are called again on the same buffers:
+ * every sum has a fixed order, and where more than the sizes fixes it, the
+ * call says so.  Elements are fp32 or bf16; bf16 is widened exactly, sums are
+ * held in fp32 (the norm in fp64) and each result is rounded once, to nearest
+ * even.  Pointers need only their element's alignment, except workspaces (16
+ * bytes); rows may be further apart than they are wide (strides in elements,
+ * never less than the width).  Offsets are 64-bit.  Outputs must not overlap inputs unless a call
  * says so; that is the caller's to keep, like the sizes of its buffers.
  * A workspace too small is HC_ERR_INSUFFICIENT_CAPACITY; its contents need
  * not be kept between calls, and a call in flight owns it.
@@ -560,6 +561,11 @@ typedef enum {
  *   hc_grad_norm: *d_norm (device fp32) = the norm.  Squares and sums are
  *     fp64, so that no finite fp32 or bf16 gradient overflows or vanishes in
  *     them; the result is rounded once to fp32.  A NaN anywhere gives NaN.
+ *     The order of the fp64 sum follows the counts, the types and where the
+ *     tensors (and outputs) lie: their places in lines of 128 bytes, and which
+ *     of them follow one another in memory.  The same values elsewhere, or
+ *     with other outputs, may so give a norm that, in rare cases, differs in
+ *     its last bit.
  *   hc_clip_grads: outs[i] = coef * grads[i] with coef = min(1, max_norm /
  *     (*d_norm + 1e-6)) in fp32 (NaN stays NaN, an infinite norm gives 0).
  *     In place where outs[i] == grads[i]; a coefficient of 1 writes nothing
@@ -599,7 +605,8 @@ hc_status_t hc_embedding(const void *ids, int id_bytes, size_t ntokens, const vo
 /*
  * hc_embedding_grad -- the table's gradient, from tokens sorted by id:
  *   dweight[v] = round(scale * sum over t with ids[t] - vocab_start == v of dout[t])
- * summed in fp32 in an order that only the ids fix.  Rows that no token has
+ * summed in fp32 in an order that the ids, ntokens and dim fix (so a table split
+ * by columns may add up in another order than the whole).  Rows that no token has
  * become zero, or with accumulate != 0 stay as they are, while the others get
  * dweight[v] + that sum (added in fp32, rounded once).
  *   padding_id: tokens of this id (counted as in ids, before vocab_start) add

@@ -696,6 +696,33 @@ def test_ids_at_the_ends_of_64_bits(start):
     assert plan.expert_counts.tolist() == [keys.count(v) for v in range(vocab)], keys
 
 
+def test_what_fixes_the_order_of_sums():
+    """The embedding gradient's bits follow the ids, the tokens and the width
+    alone, wherever the rows lie; the norm's, the tensors' places to one another
+    and in their lines."""
+    g = gen(28)
+    n, vocab, dim = 6000, 700, 200
+    ids = make_ids("falling", n, vocab, 0, torch.int64, g)
+    ws = space(hc.hc_embedding_grad_workspace_bytes(n, vocab, dim))
+    values = torch.randn((n, dim), generator=g, device="cuda")
+    got = []
+    for pad, off, idt in ((0, 0, torch.int64), (5, 3, torch.int32), (128, 1, torch.int64)):
+        _, dout = guarded((n, dim), F, dim + pad, off)
+        dout.copy_(values)
+        _, dw = guarded((vocab, dim), F, dim + pad, off)
+        hc.hc_embedding_grad(ids.to(idt), dout, dw, ws.random_(0, 256, generator=g))
+        got.append(dw.clone())
+    assert all(torch.equal(x, got[0]) for x in got[1:])
+    flat = torch.randn(2_000_000, generator=g, device="cuda")
+    norms = []
+    for buf in (flat, flat.clone()):
+        xs = [buf[3 + i * 9973:3 + i * 9973 + 9973 - i % 2] for i in range(200)]
+        d = torch.zeros(1, device="cuda")
+        hc.hc_grad_norm(xs, d, space(hc.hc_grad_norm_workspace_bytes(len(xs))))
+        norms.append(float(d))
+    assert norms[0] == norms[1]
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def step_calls(s):
