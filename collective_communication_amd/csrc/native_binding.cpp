@@ -137,6 +137,9 @@ struct Sequence {
   PyObject* operator[](size_t i) const { return PySequence_Fast_GET_ITEM(o, (Py_ssize_t)i); }
 };
 
+// Whether the elements fill their storage, once each, in any order.
+bool dense(const at::Tensor& t) { return t.is_non_overlapping_and_dense(); }
+
 Tensors tensors(const Sequence& s) {
   Tensors r;
   const size_t n = s.size();
@@ -146,8 +149,8 @@ Tensors tensors(const Sequence& s) {
   for (size_t i = 0; i < n; ++i) {
     const at::Tensor& t = tensor(s[i], "a gradient");
     r.dtypes.push_back(dtype_of(t));
+    if (!dense(t)) raise(PyExc_ValueError, "grads[%zu] is not dense: its storage has gaps", i);
     if (!t.is_cuda()) raise(PyExc_ValueError, "grads[%zu] is not a device tensor", i);
-    if (!t.is_non_overlapping_and_dense()) raise(PyExc_ValueError, "grads[%zu] is not dense: its storage has gaps", i);
     r.p.push_back(t.data_ptr());
     r.counts.push_back((size_t)t.numel());
   }
@@ -290,7 +293,7 @@ PyObject* is_dense(PyObject*, PyObject* o) {
     PyErr_SetString(PyExc_TypeError, "not a tensor");
     return nullptr;
   }
-  return PyBool_FromLong(THPVariable_Unpack(o).is_non_overlapping_and_dense());
+  return PyBool_FromLong(dense(THPVariable_Unpack(o)));
 }
 
 #define HC_METHOD(name, n) \

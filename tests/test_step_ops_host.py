@@ -258,3 +258,23 @@ def test_dense_storage_rule(hc):
         assert t.is_contiguous() or hc._dense(t)
     for t in (x[:, :2], x[..., ::2], x[:, :, :1].expand(6, 4, 5)):
         assert not t.is_contiguous() and not hc._dense(t)
+
+
+def test_operators_refuse_tensors_with_gaps(hc):
+    """The gap is what they refuse, before the place (these are host tensors);
+    without one, in any order of dimensions, it is the place."""
+    d, ws = torch.zeros(1), torch.zeros(64)
+    x = torch.zeros(6, 4, 5)
+    calls = (lambda t: hc.hc_grad_norm([t, x], d, ws), lambda t: hc.hc_clip_grads([t, x], d, 1.0, ws),
+             lambda t: hc.hc_clip_grad_norm([t, x], 1.0, d, ws))
+    gaps = (x[:, :2], x[..., ::2], x[:, :, :1].expand(6, 4, 5), x.permute(2, 0, 1)[::2], x[:, 1:3].transpose(0, 2),
+            torch.zeros(1).expand(7))
+    dense = (x, x.transpose(0, 1), x.permute(2, 0, 1), x[:1], torch.zeros(3, 1, 4).transpose(0, 1), x[2, 3])
+    for call in calls:
+        for t in gaps:
+            with pytest.raises(ValueError, match=r"grads\[0\] is not dense"):
+                call(t)
+        for t in dense:
+            assert hc._dense(t)
+            with pytest.raises(ValueError, match=r"grads\[0\] is not a device tensor"):
+                call(t)
