@@ -810,6 +810,45 @@ def test_calls_run_on_the_stream_they_are_given():
         assert torch.equal(s[o], want[o]), o
 
 
+@pytest.mark.parametrize("handle", ["stream", "raw handle"])
+def test_calls_on_a_stream_given_by_argument(handle):
+    """Every call takes stream=, and runs there in order, whichever stream is current."""
+    s, want = step_state(), step_state()
+    new_inputs(s, 51)
+    new_inputs(want, 52)
+    step_calls(want)
+    want["norm2"] = want["norm"].clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    late = {n: want[n].clone() for n in ("ids", "experts")}
+    slow = torch.zeros(1 << 27, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            slow.add_(1.0)
+        for n, x in late.items():
+            s[n].copy_(x)
+    k = {"stream": side if handle == "stream" else side.cuda_stream}
+    s["norm2"] = torch.zeros(1, device="cuda")
+    torch.cuda.current_stream().synchronize()        # s["norm2"]; the side stream is still at work
+    hc.hc_embedding(s["ids"], s["table"], s["x"], scale=1.5, **k)
+    hc.hc_expert_sort(s["experts"], s["plan"], s["ws1"], **k)
+    hc.hc_expert_dispatch(s["x"], s["plan"], s["rows"], **k)
+    hc.hc_expert_combine(s["rows"], s["plan"], s["w"], s["y"], **k)
+    hc.hc_expert_combine_grad(s["y"], s["rows"], s["plan"], s["w"], s["drows"], s["dw"], **k)
+    hc.hc_expert_combine(s["drows"], s["plan"], None, s["dx"], **k)
+    hc.hc_embedding_grad(s["ids"], s["dx"], s["dtable"], s["ws2"], scale=1.5, **k)
+    hc.hc_clip_grad_norm([s["dtable"], s["dw"]], 0.5, s["norm"], s["ws3"], outs=[s["clipped"], s["dw2"]], **k)
+    hc.hc_grad_norm([s["dtable"], s["dw"]], s["norm2"], s["ws3"], **k)
+    side.synchronize()
+    for o in OUTPUTS:
+        assert torch.equal(s[o], want[o]), o
+    assert abs(float(s["norm2"]) - float(want["norm2"])) <= 2 * U * float(want["norm2"])
+    hc.hc_clip_grads([s["dtable"], s["dw"]], s["norm"], 0.5, s["ws3"], **k)      # in place
+    side.synchronize()
+    assert torch.equal(s["dtable"], want["clipped"]) and torch.equal(s["dw"], want["dw2"])
+
+
 def test_calls_on_a_stream_of_few_compute_units():
     """No call waits for more workgroups than the stream's compute units hold."""
     s, want = step_state(), step_state()
