@@ -723,6 +723,132 @@ def test_what_fixes_the_order_of_sums():
     assert norms[0] == norms[1]
 
 
+# ------------------------------------------------------------------ rows past the caches
+
+def slices(n, per):
+    """Ranges of [0, n) of some 8 million values, `per` each."""
+    step = max(1, (1 << 23) // per)
+    return [slice(i, min(n, i + step)) for i in range(0, n, step)]
+
+
+def near(got, want, bound, what):
+    assert bool(((got.double() - want).abs() <= bound).all()), what
+
+
+LARGE_LOOKUPS = [
+    # tokens, rows, dim, type: 128 MiB of output and more
+    (33_000, 900, 1031, F),
+    (33_000, 20_011, 2051, B),
+    (540_000, 5000, 65, F),
+    (11_300_000, 1000, 3, F),
+    (13_500_000, 70_000, 5, B),
+]
+
+
+@pytest.mark.parametrize("case", LARGE_LOOKUPS, ids=lambda c: "-".join(map(str, c)))
+def test_large_lookups(case):
+    n, vocab, dim, dtype = case
+    g = gen(61)
+    ids = torch.randint(-vocab // 4, vocab + 5, (n,), generator=g, device="cuda", dtype=torch.int32)
+    _, weight = guarded((vocab, dim), dtype, dim + 3, 1)
+    weight.copy_(torch.randn((vocab, dim), generator=g, device="cuda"))
+    buf, out = guarded((n, dim), dtype, dim + 1, 3)
+    assert out.numel() * out.element_size() >= 128 << 20
+    hc.hc_embedding(ids, weight, out, scale=2.0)
+    for s in slices(n, dim):
+        k = ids[s].long()
+        there = (k >= 0) & (k < vocab)
+        want = torch.where(there[:, None], weight[k.clamp(0, vocab - 1)] * 2.0, 0.0)
+        assert torch.equal(out[s], want), s
+    check_guards(buf, out)
+
+
+LARGE_ROWS = [
+    # tokens, k, dim, type: rows by slot of 128 to 256 MiB or more, a token's side below 128 MiB or above
+    (33_000, 1, 1031, F),
+    (17_000, 4, 1031, F),
+    (33_000, 2, 2051, B),
+    (140_000, 1, 513, B),
+    (100_000, 3, 250, F),
+    (6_000_000, 2, 3, F),
+    (14_000_000, 2, 5, B),
+]
+
+
+@pytest.mark.parametrize("case", LARGE_ROWS, ids=lambda c: "-".join(map(str, c)))
+def test_large_expert_rows(case):
+    n, k, dim, dtype = case
+    g = gen(62)
+    e, every, start, align = 7, 9, 1, 4
+    first = torch.randint(0, every, (n, 1), generator=g, device="cuda", dtype=torch.int32)
+    ids = (first + torch.arange(k, device="cuda", dtype=torch.int32) * 2) % every
+    plan = hc.ExpertPlan.for_sizes(n, k, e, align)
+    hc.hc_expert_sort(ids, plan, space(hc.hc_expert_sort_workspace_bytes(n * k, e)), expert_start=start)
+    row, slot, used = plan.row_of_slot.view(n, k), plan.slot_of_row, int(plan.expert_offsets[-1])
+    here = (ids >= start) & (ids < start + e)
+    assert torch.equal(row >= 0, here) and int(here.sum()) == int((slot >= 0).sum())
+    placed = torch.where(here, row, 0).view(-1).long()
+    assert torch.equal(slot[placed[here.view(-1)]], here.view(-1).nonzero()[:, 0].int())
+    assert n * k * dim * (4 if dtype == F else 2) >= 128 << 20
+    x = guarded((n, dim), dtype, dim + 1, 1)[1]
+    x.copy_(torch.randn((n, dim), generator=g, device="cuda", dtype=dtype))
+    # dispatch
+    buf, rows = guarded((plan.rows, dim), dtype, dim + 3, 3)
+    hc.hc_expert_dispatch(x, plan, rows)
+    for s in slices(used, dim):
+        want = torch.where((slot[s] >= 0)[:, None], x[(slot[s].long() // k).clamp(min=0)], 0.0)
+        assert torch.equal(rows[s], want), s
+    assert bool((rows[used:] == GUARD).all())
+    check_guards(buf, rows)
+    # combine; what no slot has is NaN, which must not be read
+    rows.copy_(torch.randn((plan.rows, dim), generator=g, device="cuda", dtype=dtype))
+    rows[slot < 0] = math.nan
+    weights = torch.rand((n, k), generator=g, device="cuda")
+    buf, out = guarded((n, dim), dtype, dim + 1, 1)
+    for w in (weights, None):
+        hc.hc_expert_combine(rows, plan, w, out)
+        for s in slices(n, k * dim):
+            picked = torch.where(here[s][..., None], rows[row[s].long().clamp(min=0)].double(), 0.0)
+            terms = picked * (w[s].double()[..., None] if w is not None else 1.0)
+            want = terms.sum(1)
+            near(out[s], want, terms.abs().sum(1) * k * U + want.abs() * HALF[dtype] + TINY[dtype], ("combine", s))
+    check_guards(buf, out)
+    del buf, out
+    # the gradient of combine, of x as the output's
+    buf, drows = guarded((plan.rows, dim), dtype, dim + 1, 1)
+    wbuf, dweights = guarded((n * k,), F)
+    hc.hc_expert_combine_grad(x, rows, plan, weights, drows, dweights)
+    by_slot = weights.view(-1)
+    for s in slices(used, dim):
+        at = slot[s].long().clamp(min=0)
+        want = torch.where((slot[s] >= 0)[:, None], x[at // k].double() * by_slot[at].double()[:, None], 0.0)
+        near(drows[s], want, want.abs() * (U + HALF[dtype]) + TINY[dtype], ("drows", s))
+    assert bool((drows[used:] == GUARD).all())
+    for s in slices(n, k * dim):
+        prod = torch.where(here[s][..., None], rows[row[s].long().clamp(min=0)].double(), 0.0) * x[s].double()[:, None]
+        near(dweights.view(n, k)[s], prod.sum(2), prod.abs().sum(2) * dim * U + TINY[F], ("dweights", s))
+    check_guards(buf, drows)
+    check_guards(wbuf, dweights)
+
+
+@pytest.mark.parametrize("types", [(F, F), (B, B)], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(700, 300, 9001), (9000, 1500, 8195), (300, 1500, 24_001), (200, 40, 70_003)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_gradient_of_wide_rows_that_lie_apart(case, types):
+    """Tables of few wide rows with something between them, which the zeroing
+    beside the sort takes row by row.  Sums of small integers are exact."""
+    n, vocab, dim = case
+    dt, wt = types
+    g = gen(63)
+    ids = make_ids("falling", n, vocab, 0, torch.int32, g)
+    dout = torch.randint(-2, 3, (n, dim), generator=g, device="cuda").to(dt)
+    want = torch.zeros((vocab, dim), device="cuda").index_add_(0, ids.long(), dout.float())
+    buf, dw = guarded((vocab, dim), wt, dim + 5, 1)
+    hc.hc_embedding_grad(ids, dout, dw, space(hc.hc_embedding_grad_workspace_bytes(n, vocab, dim)))
+    assert torch.equal(dw, want.to(wt))
+    check_guards(buf, dw)
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def step_calls(s):
