@@ -186,6 +186,19 @@ def test_norm_of_extreme_and_special_values():
     assert norm == 0.0 and outs[0].tolist() == [0.0] * 9
 
 
+@pytest.mark.parametrize("dtype", [F, B])
+def test_clipping_of_the_smallest_values(dtype):
+    """Gradients among the smallest numbers are scaled, not flushed."""
+    x = torch.tensor([1e-38, 2e-40, -3e-40, 9.2e-41, -9.2e-41, 0.0], device="cuda").to(dtype)
+    assert int((x != 0).sum()) == 5
+    norm, outs = clip([x], 1.0)
+    assert norm > 0 and torch.equal(outs[0], x)                 # a coefficient of 1
+    norm, outs = clip([x], 3e-7)
+    want = x.double().cpu() * (3e-7 / (norm64([x]) + 1e-6))
+    close(outs[0], want, want.abs() * (5.1 * U + HALF[dtype]) + TINY[dtype])
+    assert bool((outs[0][:3] != 0).all())
+
+
 def test_clip_by_a_norm_of_more_than_these_tensors():
     """Two ranks' shards: each clips by the norm of both."""
     a, b = (torch.randn(5000, generator=gen(s), device="cuda") for s in (3, 4))
@@ -721,6 +734,67 @@ def test_what_fixes_the_order_of_sums():
         hc.hc_grad_norm(xs, d, space(hc.hc_grad_norm_workspace_bytes(len(xs))))
         norms.append(float(d))
     assert norms[0] == norms[1]
+
+
+# ------------------------------------------------------------------ with the exchange
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_a_table_split_over_ranks(dtype):
+    """Each rank looks up its part of the vocabulary and hc_allreduce adds the
+    rows, which gives the whole table's; each rank's gradient is its part of
+    the whole one."""
+    g = gen(71)
+    n, vocab, dim = 501, 1000, 136
+    weight = torch.randn((vocab, dim), generator=g, device="cuda").to(dtype)
+    dout = torch.randn((n, dim), generator=g, device="cuda").to(dtype)
+    ids = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    ws = space(hc.hc_embedding_grad_workspace_bytes(n, vocab, dim))
+    whole, dwhole = torch.empty_like(dout), torch.empty_like(weight)
+    hc.hc_embedding(ids, weight, whole, scale=0.3)
+    hc.hc_embedding_grad(ids, dout, dwhole, ws, scale=0.3)
+    cuts, outs = (0, 334, 667, vocab), []
+    for a, b in zip(cuts, cuts[1:]):
+        outs.append(torch.full_like(dout, GUARD))
+        hc.hc_embedding(ids, weight[a:b], outs[-1], vocab_start=a, scale=0.3)
+        part = torch.full((b - a, dim), GUARD, dtype=dtype, device="cuda")
+        hc.hc_embedding_grad(ids, dout, part, ws, vocab_start=a, scale=0.3)
+        k = ids[(ids >= a) & (ids < b)] - a
+        terms = torch.zeros(b - a, device="cuda").index_add_(0, k, torch.ones(len(k), device="cuda"))[:, None]
+        mags = torch.zeros((b - a, dim), device="cuda").index_add_(0, k, dout[(ids >= a) & (ids < b)].float().abs())
+        # the same terms in another order: twice the order's bound and the result's two roundings
+        near(part, dwhole[a:b].double(), 2 * (0.3 * mags * (terms + 2) * U + dwhole[a:b].double().abs() *
+                                              (U + HALF[dtype]) + TINY[dtype]), (a, b))
+    hc.hc_allreduce(outs, outs)
+    assert all(torch.equal(o, whole) for o in outs)             # a row and zeroes: exact
+
+
+def test_experts_split_over_ranks():
+    """Each rank lays out, runs and combines its experts' rows, and
+    hc_allreduce adds the ranks' sums, which gives all experts'."""
+    g = gen(72)
+    n, k, every, dim, ranks = 300, 4, 12, 72, 3
+    x = torch.randn((n, dim), generator=g, device="cuda")
+    ids = torch.rand((n, every), generator=g, device="cuda").topk(k, dim=1).indices
+    ids[5] = -1                                                 # a masked token
+    w = torch.rand((n, k), generator=g, device="cuda")
+    gain = torch.randn((every, dim), generator=g, device="cuda")    # expert e scales its rows
+    parts = []
+    for r in range(ranks):
+        e = every // ranks
+        plan = hc.ExpertPlan.for_sizes(n, k, e, 16)
+        hc.hc_expert_sort(ids, plan, expert_start=r * e)
+        rows = torch.zeros((plan.rows, dim), device="cuda")
+        hc.hc_expert_dispatch(x, plan, rows)
+        ends = plan.expert_offsets.tolist()
+        for i in range(e):
+            rows[ends[i]:ends[i + 1]] *= gain[r * e + i]
+        parts.append(torch.full((n, dim), GUARD, device="cuda"))
+        hc.hc_expert_combine(rows, plan, w, parts[-1])
+    hc.hc_allreduce(parts, parts)
+    terms = torch.where((ids >= 0)[..., None], x.double()[:, None] * gain.double()[ids.clamp(min=0)], 0.0) * w[..., None]
+    # a product in the rows, k in the sums, one addition per rank
+    near(parts[0], terms.sum(1), terms.abs().sum(1) * (1 + k + ranks) * U + TINY[F], "sum")
+    assert all(torch.equal(p, parts[0]) for p in parts[1:]) and not bool(parts[0][5].any())
 
 
 # ------------------------------------------------------------------ rows past the caches
