@@ -15,7 +15,7 @@
 // the sum and join launches, which look their rows up in the sorted list.
 //
 // Measured: the lookup of 30,011 x 4096 bf16, a quarter of them in the table,
-// 40 us (246 MB written, 7.5 TB/s); the gradient of 32,768 x 2048 bf16 into
+// 41 us (246 MB written, 37 read, 6.9 TB/s); the gradient of 32,768 x 2048 bf16 into
 // 100,003 fp32 rows 194 us, of which the sort 24 (41 with 200 MB zeroed
 // beside it): 1.0 GB in all, 0.85 of it written, 5.2 TB/s, as a large copy
 // does.  Its parts alone: the sums 60-75 us, all the zeroing 117 us.
@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
 // and depend on nothing but the ids; the other compute units meanwhile zero
 // the first rows of the table, tokens or not (the sums come later and write
 // theirs again).  Pieces of some 64 KB: of one flat range where the rows are
-// contiguous, else whole rows.  A launch of the sort takes 2-3 us longer for 25
+// contiguous, else whole rows, a wave to each; a row wider than that is a piece
+// by itself (500 x 65,536 bf16 into 600 fp32 rows: 75 us contiguous, 86 apart).  A launch of the sort takes 2-3 us longer for 25
 // MB of them and 5 us for 50 MB, which alone would take 8 (2000 tokens x 1000
 // fp32 into 10,007 rows, 40 MB: 23.4 us without, 18.3 with).
 constexpr uint64_t kPieceBytes = 65536;
@@ -233,7 +234,8 @@ size_t sort_ids_ws_bytes(size_t n) {
 
 namespace {
 
-// Pieces that a launch of the sort zeroes beside it, 50 MB.  The gradient with
+// Pieces that a launch of the sort zeroes beside it, 50 MB (more where rows that
+// lie apart are wider than a piece: 200 MB of 256 KB rows).  The gradient with
 // 25, 50, 100 and 200 MB a launch, us: 32,768 x 2048 bf16 into 100,003 fp32 rows
 // 202, 196, 198 and 228; 16,000 into 40,000 rows 92, 92, 106 and 113; placed by one
 // launch, 8000 into 128,000 rows 210, 210, 212 and 213, 500 into 30,000 47, 47, 49
@@ -310,7 +312,9 @@ struct Grad {
 
 // Writes N columns of a table row from `at` on; the first `skip` of them
 // belong to another lane, which has the same sums for them: written all the
-// same, unless the table's own values are added.
+// same, unless the table's own values are added: that goes by elements, which
+// is slow (32,768 x 2048 bf16 into 100,003 fp32 rows 286 us, where overwriting takes
+// 196 and these rows read and written, 592 MB, some 114).
 template <typename To, int N, bool ACC>
 __device__ __forceinline__ void write_row(const Grad& g, uint32_t row, uint32_t at, uint32_t skip, const float* sum) {
   typename To::raw* p = elem<To>(g.dweight, (size_t)row * g.wstride + at);

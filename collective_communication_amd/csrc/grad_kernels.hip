@@ -42,7 +42,10 @@ constexpr uint32_t kStreamChunks = (uint32_t)(kStreamStoreBytes / kChunkBytes);
 // for it, until from here on they only push each other out.  Both passes on
 // bf16 values, plain / non-temporal, us: 67 MB 40.7 / 38.9, 101 MB 57.1 / 55.5,
 // 134 MB 65.7 / 70.0, 268 MB 126 / 134, 403 MB 193 / 198, 537 MB 265 / 263,
-// 1.07 GB 549 / 531.
+// 1.07 GB 549 / 531.  hc_grad_norm reads by the same rule, for the hc_clip_grads
+// that follows it (134 MB 67 / 71, 268 MB 126 / 135, 403 MB 195 / 200, 500 MB 246 /
+// 246 together); by itself it would be faster non-temporal (134 MB 27.7 / 25.5,
+// 268 MB 48.6 / 44.3, 403 MB 71 / 64; the input just written 27 / 27, 58 / 49, 93 / 73).
 constexpr uint32_t kStreamLoadChunks = (512u << 20) / kChunkBytes;
 // Up to here the clipping launch has at most kMaxGrid workgroups, which add the
 // partials up themselves; above it has one per chunk.
