@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(KeySource src, size
 // the first rows of the table, tokens or not (the sums come later and write
 // theirs again).  Pieces of some 64 KB: of one flat range where the rows are
 // contiguous, else whole rows, a wave to each; a row wider than that is a piece
-// by itself (500 x 65,536 bf16 into 600 fp32 rows: 75 us contiguous, 86 apart).  A launch of the sort takes 2-3 us longer for 25
-// MB of them and 5 us for 50 MB, which alone would take 8 (2000 tokens x 1000
-// fp32 into 10,007 rows, 40 MB: 23.4 us without, 18.3 with).
+// by itself (500 x 65,536 bf16 into 600 fp32 rows: 75 us contiguous, 86 apart).
+// A launch of the sort takes 2-3 us longer for 25 MB of them and 5 us for 50 MB,
+// which alone would take 8 (2000 tokens x 1000 fp32 into 10,007 rows, 40 MB:
+// 23.4 us without, 18.3 with).
 constexpr uint64_t kPieceBytes = 65536;
 
 struct ZeroJob {
