@@ -41,6 +41,11 @@ HC_BLOCK_ELEMS = 16384
 HC_MAX_RANKS = 64
 HC_MAX_TOPK = 64
 HC_MAX_EXPERTS = 1024
+HC_MAX_GROUPS = 64
+HC_MAX_NORM_DIM = 32768
+HC_STATE_BLOCK = 128
+HC_SCORES_SOFTMAX = 0
+HC_SCORES_SIGMOID = 1
 
 EXPORTED = [
     "hc_allreduce", "hc_reduce_scatter", "hc_all_gather", "hc_compress_bound_bf16",
@@ -53,7 +58,8 @@ EXPORTED = [
     "hc_grad_norm_workspace_bytes", "hc_grad_norm", "hc_clip_grads", "hc_clip_grad_norm", "hc_embedding",
     "hc_embedding_grad_workspace_bytes", "hc_embedding_grad", "hc_expert_rows_bound",
     "hc_expert_sort_workspace_bytes", "hc_expert_sort", "hc_expert_dispatch", "hc_expert_combine",
-    "hc_expert_combine_grad",
+    "hc_expert_combine_grad", "hc_rms_norm", "hc_rms_norm_8bit", "hc_rms_norm_grad_workspace_bytes",
+    "hc_rms_norm_grad", "hc_route", "hc_route_grad", "hc_adamw_table_bytes", "hc_adamw_plan", "hc_adamw",
 ]
 
 
@@ -80,6 +86,25 @@ class hc_expert_plan_t(ctypes.Structure):
                 ("row_align", ctypes.c_int32), ("rows", ctypes.c_size_t), ("row_of_slot", ctypes.c_void_p),
                 ("slot_of_row", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
                 ("expert_counts", ctypes.c_void_p)]
+
+
+class hc_route_opts_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("scores", ctypes.c_int32), ("ngroups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class hc_adamw_plan_t(ctypes.Structure):
+    _fields_ = [("ntensors", ctypes.c_size_t), ("chunks", ctypes.c_uint64), ("state_bits", ctypes.c_int32),
+                ("d_table", ctypes.c_void_p)]
+
+
+class hc_adamw_opts_t(ctypes.Structure):
+    _fields_ = [("step", ctypes.c_int64), ("lr", ctypes.c_double), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("grad_scale", ctypes.c_float), ("max_norm", ctypes.c_float), ("d_norm", ctypes.c_void_p),
+                ("d_lr", ctypes.c_void_p), ("d_step", ctypes.c_void_p), ("seed", ctypes.c_uint64),
+                ("skip_nonfinite", ctypes.c_int32)]
 
 
 _lib = None
@@ -136,8 +161,19 @@ def load(path: str = LIB_PATH):
     L.hc_expert_dispatch.argtypes = [P, I, S, S, PE, P, S, P]
     L.hc_expert_combine.argtypes = [P, I, S, S, PE, P, P, S, P]
     L.hc_expert_combine_grad.argtypes = [P, I, S, S, P, S, PE, P, P, S, P, P]
+    PO, PA, PB = ctypes.POINTER(hc_route_opts_t), ctypes.POINTER(hc_adamw_plan_t), ctypes.POINTER(hc_adamw_opts_t)
+    PF = ctypes.POINTER(F)
+    L.hc_rms_norm.argtypes = [P, I, S, S, S, P, S, P, I, F, P, S, P, S, P]
+    L.hc_rms_norm_8bit.argtypes = [P, I, S, S, S, P, S, P, I, F, P, S, P, S, I, P, S, P]
+    L.hc_rms_norm_grad_workspace_bytes.argtypes = [S, S]
+    L.hc_rms_norm_grad.argtypes = [P, I, S, S, S, P, S, P, I, F, P, S, P, S, P, I, I, P, S, P]
+    L.hc_route.argtypes = [P, I, S, I, S, PO, P, P, P]
+    L.hc_route_grad.argtypes = [P, I, S, I, S, PO, P, P, P, S, P]
+    L.hc_adamw_table_bytes.argtypes = [S]
+    L.hc_adamw_plan.argtypes = [PA, PP, PP, PP, PP, PP, PP, PP, PF, PS, PI, PI, S, P, S, P]
+    L.hc_adamw.argtypes = [PA, PB, P]
     for name in ("hc_grad_norm_workspace_bytes", "hc_embedding_grad_workspace_bytes", "hc_expert_rows_bound",
-                 "hc_expert_sort_workspace_bytes"):
+                 "hc_expert_sort_workspace_bytes", "hc_rms_norm_grad_workspace_bytes", "hc_adamw_table_bytes"):
         getattr(L, name).restype = S
     L.hc_step_count.argtypes = [I, I]
     L.hc_step_count.restype = I
@@ -149,7 +185,8 @@ def load(path: str = LIB_PATH):
                  "hc_decompress_bf16_entropy", "hc_compressed_allreduce", "hc_stream_create_cu_budget",
                  "hc_stream_destroy", "hc_cu_census", "hc_stream_create_cu_range", "hc_grad_norm", "hc_clip_grads",
                  "hc_clip_grad_norm", "hc_embedding", "hc_embedding_grad", "hc_expert_sort", "hc_expert_dispatch",
-                 "hc_expert_combine", "hc_expert_combine_grad"):
+                 "hc_expert_combine", "hc_expert_combine_grad", "hc_rms_norm", "hc_rms_norm_8bit",
+                 "hc_rms_norm_grad", "hc_route", "hc_route_grad", "hc_adamw_plan", "hc_adamw"):
         getattr(L, name).restype = I
     L.hc_status_string.argtypes = [I]
     L.hc_status_string.restype = ctypes.c_char_p
@@ -650,6 +687,135 @@ def hc_expert_combine_grad(dout: torch.Tensor, rows: torch.Tensor, plan: ExpertP
     """The gradients of hc_expert_combine: drows by row, dweights by slot."""
     st = (_native or _load_native()).expert_combine_grad(dout, rows, plan._at, weights, drows, dweights,
                                                          _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+def hc_rms_norm(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *, residual: torch.Tensor | None = None,
+                sum_out: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """out = h / sqrt(mean(h^2) + eps) * weight by rows, h = x + residual,
+    which sum_out receives; see include/hc.h."""
+    st = (_native or _load_native()).rms_norm(x, weight, out, residual, sum_out, eps, _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+def hc_rms_norm_8bit(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, scales: torch.Tensor, *,
+                     group: int = 0, residual: torch.Tensor | None = None, sum_out: torch.Tensor | None = None,
+                     eps: float = 1e-6, stream=None):
+    """hc_rms_norm with rows of 8 bits (float8_e4m3fn, or uint8 for the bytes)
+    and a scale for each group of columns (0: for each row)."""
+    st = (_native or _load_native()).rms_norm_8bit(x, weight, out, scales, group, residual, sum_out, eps,
+                                                   _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+def hc_rms_norm_grad_workspace_bytes(ntokens: int, dim: int) -> int:
+    return int(load().hc_rms_norm_grad_workspace_bytes(ntokens, dim))
+
+
+def hc_rms_norm_grad(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dx: torch.Tensor,
+                     dweight: torch.Tensor | None = None, ws: torch.Tensor | None = None, *,
+                     dsum: torch.Tensor | None = None, eps: float = 1e-6, accumulate: bool = False, stream=None):
+    """The gradients of hc_rms_norm by its h (dsum, what arrives there beside
+    the norm's, is added) and by its weight (added to dweight when accumulate;
+    not computed when dweight is None, nor is ws needed then)."""
+    st = (_native or _load_native()).rms_norm_grad(dout, h, weight, dx, dweight, ws, dsum, eps, accumulate,
+                                                   _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+_SCORES = {"softmax": HC_SCORES_SOFTMAX, "sigmoid": HC_SCORES_SIGMOID}
+
+
+def _scores_kind(scores: str) -> int:
+    if scores not in _SCORES:
+        raise ValueError(f"scores {scores!r} is none of {', '.join(_SCORES)}")
+    return _SCORES[scores]
+
+
+def hc_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, *, scores: str = "softmax",
+             bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1, group_best: int = 1,
+             renormalise: bool = True, scale: float = 1.0, stream=None):
+    """Each token's k experts (int32, (tokens, k)) and weights (float32) from
+    its logits: scores, a bias on the choice, the best groups, the k best of
+    them; see include/hc.h."""
+    st = (_native or _load_native()).route(logits, experts, weights, _scores_kind(scores), bias, groups, top_groups,
+                                           group_best, renormalise, scale, _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+def hc_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor, dlogits: torch.Tensor, *,
+                  scores: str = "softmax", renormalise: bool = True, scale: float = 1.0, stream=None):
+    """The gradient of hc_route's weights by the logits, the choice held."""
+    st = (_native or _load_native()).route_grad(logits, experts, dweights, dlogits, _scores_kind(scores), renormalise,
+                                                scale, _raw_stream(stream))
+    if st:
+        _check(st)
+
+
+def hc_adamw_table_bytes(ntensors: int) -> int:
+    return int(load().hc_adamw_table_bytes(ntensors))
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step (hc_adamw_plan_t) and their table on the
+    device, for as long as the tensors stay where they are.  Gradients, states
+    and copies have the shape and strides of their parameter, which may have
+    any order of dimensions but no gaps.  The plan keeps its tensors alive.
+
+    States of 32 bits are float32; with m_scales and v_scales they are 8 bits
+    (float8_e4m3fn or uint8 codes), a float32 scale for every HC_STATE_BLOCK
+    values.  copies: bfloat16 copies of float32 parameters, or None each.
+    decays: factors of the weight decay.  ``for_params`` makes zero states."""
+
+    def __init__(self, params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_scales=None, copies=None, decays=None,
+                 table: torch.Tensor | None = None, stream=None):
+        native = _native or _load_native()
+        self.params, self.grads = list(params), list(grads)
+        self.exp_avgs, self.exp_avg_sqs = list(exp_avgs), list(exp_avg_sqs)
+        self.m_scales = None if m_scales is None else list(m_scales)
+        self.v_scales = None if v_scales is None else list(v_scales)
+        self.copies = None if copies is None else list(copies)
+        if table is None:
+            device = self.params[0].device if self.params else "cuda"
+            table = torch.empty(hc_adamw_table_bytes(len(self.params)), dtype=torch.uint8, device=device)
+        self.table = table
+        self._c = hc_adamw_plan_t()
+        self._at = ctypes.addressof(self._c)
+        st = native.adamw_plan(self._at, self.params, self.grads, self.exp_avgs, self.exp_avg_sqs, self.m_scales,
+                               self.v_scales, self.copies, decays, table, _raw_stream(stream))
+        if st:
+            _check(st)
+
+    @classmethod
+    def for_params(cls, params, grads, *, state_bits: int = 32, copies=None, decays=None, stream=None):
+        """A plan with states as they are before the first step."""
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits {state_bits} is neither 8 nor 32")
+        params = list(params)
+        dtype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        like = lambda p: torch.empty_like(p, dtype=dtype).zero_()  # noqa: E731
+        scales = lambda p: torch.zeros(-(-p.numel() // HC_STATE_BLOCK), device=p.device)  # noqa: E731
+        more = {} if state_bits == 32 else {"m_scales": [scales(p) for p in params],
+                                            "v_scales": [scales(p) for p in params]}
+        return cls(params, grads, [like(p) for p in params], [like(p) for p in params], copies=copies, decays=decays,
+                   stream=stream, **more)
+
+
+def hc_adamw(plan: AdamWPlan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+             grad_scale: float = 1.0, d_norm: torch.Tensor | None = None, max_norm: float = 1.0, seed: int = 0,
+             skip_nonfinite: bool = False, stream=None):
+    """One AdamW step of a plan's tensors; see include/hc.h.  step and lr are
+    numbers, or device scalars (int64, float32) that a captured launch follows.
+    The gradients are scaled by grad_scale and, with d_norm (their norm before
+    that), clipped to max_norm.  seed: 0 rounds to nearest, else 8-bit states
+    and bf16 parameters are rounded by random bits."""
+    st = (_native or _load_native()).adamw(plan._at, step, lr, betas[0], betas[1], eps, weight_decay, grad_scale,
+                                           d_norm, max_norm, seed, skip_nonfinite, _raw_stream(stream))
     if st:
         _check(st)
 

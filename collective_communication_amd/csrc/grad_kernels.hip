@@ -118,21 +118,6 @@ __global__ void __launch_bounds__(kThreads) table_kernel(Packed b, uint32_t n, u
   }
 }
 
-// The tensor that holds chunk c, the last whose first chunk is not after it:
-// a search over 64 places at a time, one per lane, so two loads in turn find
-// it among 4096 tensors.  Every lane of the wave calls it.
-__device__ __forceinline__ uint32_t find(const uint32_t* first, uint32_t n, uint32_t c) {
-  uint32_t lo = 0;
-  while (n > 1) {
-    const uint32_t step = (n + 63) / 64, at = lane_id() * step;
-    const uint64_t not_after = __ballot(at < n && first[lo + at] <= c);
-    const uint32_t skip = ((uint32_t)__popcll(not_after) - 1) * step;
-    lo += skip;
-    n = n - skip < step ? n - skip : step;
-  }
-  return first_lane_read(lo);
-}
-
 template <bool INF>
 __device__ __forceinline__ double join(double a, double b) {
   if constexpr (INF) return (a > b || a != a) ? a : b;
@@ -187,7 +172,7 @@ struct Place {
 // OUT: counted from the output's line, else from the input's.
 template <bool OUT>
 __device__ __forceinline__ Place place_of(const Entry* e, const uint32_t* first, uint32_t n, uint32_t c) {
-  const uint32_t t = find(first, n, c);
+  const uint32_t t = find_tensor(first, n, c);
   const Entry x = e[t];
   Place p;
   p.src = x.src;

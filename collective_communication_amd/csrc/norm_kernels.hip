@@ -1,0 +1,490 @@
+// norm_kernels.hip -- the root-mean-square norm of rows after a residual's
+// addition, with rows of their own type or of 8 bits, and its gradient, for
+// gfx950.
+//
+//   h = round(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = round(h r w)
+//   8 bits: t = h w, a = largest |t| of a group, q = e4m3(t (448 / a)), scale = a r / 448
+//   dx = round(r (dy w - h r^2 mean(dy w h)) + dsum),  dw = sum over rows of dy h r
+//
+// All are streams over rows: a row is loaded once into the registers of as many
+// lanes as its width has vectors for (8 to 64 of a wave, or 4 or 16 waves), its
+// sums are joined there, and it is written from there.  The gradient of the
+// weight is summed over a workgroup's rows in registers and left as one row of
+// partials per workgroup, which a second launch adds in a fixed order.
+#include "launch.hpp"
+#include "rows.hpp"
+#include "step_launch.hpp"
+
+namespace hc {
+namespace {
+
+constexpr uint32_t kMaxBlocks = 1u << 22;
+constexpr uint32_t kPartials = 1024;         // workgroups that leave a row of partial sums
+
+struct Norm {
+  const void* x;
+  size_t xstride;
+  const void* residual;      // or the gradient that arrives at h
+  size_t rstride;
+  const void* weight;
+  void* sum;
+  size_t sstride;
+  void* out;
+  size_t ostride;
+  float* scales;
+  size_t cstride;
+  const void* dout;
+  size_t dstride;
+  float* partials;           // NULL: no gradient of the weight
+  size_t ntokens;
+  uint32_t dim, group, groups;   // group: columns, the row's width or more for one
+  uint32_t wbf16;
+  float eps, width;          // the row's width
+};
+
+template <uint32_t LPR>
+constexpr uint32_t threads_of() {
+  return LPR > kThreads ? LPR : kThreads;
+}
+
+// The N weights from column c on.
+template <typename T>
+__device__ __forceinline__ void load_weight(const Norm& n, uint32_t c, float* w) {
+  constexpr int N = T::kVec;
+  if (n.wbf16) {
+    if constexpr (N == 4) {
+      typedef uint32_t vec2_u __attribute__((ext_vector_type(2), aligned(2)));
+      const vec2_u v = *reinterpret_cast<const vec2_u*>(elem<BF16>(n.weight, c));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[2 * i] = bits_f32(v[i] << 16);
+        w[2 * i + 1] = bits_f32(v[i] & 0xFFFF0000u);
+      }
+    } else if constexpr (N == 8) {
+      BF16::unpack(load_vec<BF16>(elem<BF16>(n.weight, c)), w);
+    } else {
+      w[0] = BF16::widen(*elem<BF16>(n.weight, c));
+    }
+  } else {
+    if constexpr (N == 1) {
+      w[0] = F32::widen(*elem<F32>(n.weight, c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) F32::unpack(load_vec<F32>(elem<F32>(n.weight, c + i)), w + i);
+    }
+  }
+}
+
+struct Add {
+  static __device__ __forceinline__ float join(float a, float b) { return a + b; }
+};
+struct Max {
+  static __device__ __forceinline__ float join(float a, float b) { return a > b ? a : b; }
+};
+
+// v joined over `lanes` (a power of two, at most 64) neighbouring lanes.
+template <typename Op>
+__device__ __forceinline__ float join_lanes(float v, uint32_t lanes) {
+  for (uint32_t m = 1; m < lanes; m <<= 1) v = Op::join(v, __shfl_xor(v, (int)m));
+  return v;
+}
+// Two values joined over the LPR lanes of a row, in all of them.  lds: a
+// workgroup's, another part for each call until a barrier.
+template <uint32_t LPR, typename A, typename B>
+__device__ __forceinline__ void join_row(float& a, float& b, float* lds) {
+  a = join_lanes<A>(a, LPR < 64 ? LPR : 64);
+  b = join_lanes<B>(b, LPR < 64 ? LPR : 64);
+  if constexpr (LPR > 64) {
+    constexpr uint32_t W = LPR / 64;
+    if (lane_id() == 0) {
+      lds[threadIdx.x >> 6] = a;
+      lds[W + (threadIdx.x >> 6)] = b;
+    }
+    __syncthreads();
+    a = lds[0];
+    b = lds[W];
+#pragma unroll
+    for (uint32_t w = 1; w < W; ++w) {
+      a = A::join(a, lds[w]);
+      b = B::join(b, lds[W + w]);
+    }
+  }
+}
+
+// 1 / sqrt(mean of squares + eps).  Where the squares pass what fp32 holds they
+// are summed once more, of values 2^80 smaller: again() does.
+template <uint32_t LPR, typename Again>
+__device__ __forceinline__ float inverse(const Norm& n, float squares, Again again) {
+  const bool past = squares == __builtin_inff();
+  const float r = 1.0f / sqrtf(squares / n.width + n.eps);
+  if (!(LPR > 64 ? past : (bool)__any(past))) return r;
+  const float small = again();
+  return past ? 0x1p-80f / sqrtf(small / n.width + n.eps * 0x1p-80f * 0x1p-80f) : r;
+}
+
+// N e4m3 codes, nearest.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* f, uint32_t skip) {
+  if constexpr (N == 1) {
+    *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[0], 0, false);
+  } else {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], lo, true);
+    }
+    if (skip == 0) {
+      if constexpr (N == 4) {
+        typedef uint32_t word_u __attribute__((aligned(1)));
+        *reinterpret_cast<word_u*>(p) = w[0];
+      } else {
+        typedef uint32_t vec2_u __attribute__((ext_vector_type(2), aligned(1)));
+        *reinterpret_cast<vec2_u*>(p) = vec2_u{w[0], w[1]};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((uint32_t)i >= skip) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+}
+
+template <typename T, int U>
+__device__ __forceinline__ float small_squares(const typename T::vec* v, const uint32_t* skip) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float h[T::kVec];
+    T::unpack(v[u], h);
+#pragma unroll
+    for (int i = 0; i < T::kVec; ++i) {
+      const float x = h[i] * 0x1p-80f;
+      sum += (uint32_t)i >= skip[u] ? x * x : 0.0f;
+    }
+  }
+  return sum;
+}
+
+// Q8: rows of 8 bits.  LPR lanes have a row, U vectors each.
+template <typename T, uint32_t LPR, int U, bool Q8>
+__global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
+  constexpr int N = T::kVec;
+  constexpr uint32_t RPW = threads_of<LPR>() / LPR;
+  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
+  const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  uint32_t turn = 0;
+  for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += (size_t)gridDim.x * RPW) {
+    const bool there = first + slot < n.ntokens;
+    const size_t t = there ? first + slot : n.ntokens - 1;    // a spare slot computes the last row and writes nothing
+    typename T::vec v[U], add[U];
+    uint32_t at[U], skip[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t c = (u * LPR + lane) * N;
+      at[u] = c < n.dim ? vec_at<T>(c, n.dim) : 0;
+      skip[u] = c < n.dim ? c - at[u] : N;                    // a vector moved back counts its own elements only
+      v[u] = zero_vec<T>();
+      if (c < n.dim) v[u] = load_vec<T>(elem<T>(n.x, t * n.xstride + at[u]));
+    }
+    if (n.residual) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        add[u] = zero_vec<T>();
+        if (skip[u] < N) add[u] = load_vec<T>(elem<T>(n.residual, t * n.rstride + at[u]));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float a[N], b[N];
+        T::unpack(v[u], a);
+        T::unpack(add[u], b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] += b[i];
+        v[u] = T::pack(a);
+      }
+    }
+    float squares = 0.0f, top = 0.0f;
+    float peak[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float h[N];
+      T::unpack(v[u], h);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float s = __builtin_fmaf(h[i], h[i], squares);
+        squares = (uint32_t)i >= skip[u] ? s : squares;
+      }
+      peak[u] = 0.0f;
+      if constexpr (Q8) {
+        if (skip[u] < N) {
+          float w[N];
+          load_weight<T>(n, at[u], w);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if ((uint32_t)i >= skip[u]) peak[u] = Max::join(fabsf(h[i] * w[i]), peak[u]);
+        }
+        top = Max::join(peak[u], top);
+      }
+    }
+    join_row<LPR, Add, Max>(squares, top, lds[turn]);
+    turn ^= 1;
+    const float r = inverse<LPR>(n, squares, [&] {
+      float sum = small_squares<T, U>(v, skip), none = 0.0f;
+      join_row<LPR, Add, Add>(sum, none, lds[turn]);
+      turn ^= 1;
+      return sum;
+    });
+    if constexpr (Q8) {
+      const uint32_t lanes = min(n.group / N, min(LPR, 64u));
+#pragma unroll
+      for (int u = 0; u < U; ++u) peak[u] = n.groups > 1 ? join_lanes<Max>(peak[u], lanes) : top;
+    }
+    if (!there) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (skip[u] == N) continue;
+      float h[N], w[N];
+      if (n.sum) store_vec<T>(elem<T>(n.sum, t * n.sstride + at[u]), v[u]);
+      T::unpack(v[u], h);
+      load_weight<T>(n, at[u], w);
+      if constexpr (Q8) {
+        // a group of tiny values is brought up first, so that 448 / a stays finite
+        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : 1.0f;
+        const float inv = peak[u] > 0.0f ? 448.0f / (peak[u] * lift) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = h[i] * w[i] * lift * inv;
+        store_codes<N>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
+        const uint32_t c = at[u] + skip[u];
+        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = peak[u] * r / 448.0f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = h[i] * r * w[i];
+        store_vec<T>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(h));
+      }
+    }
+  }
+}
+
+// x is h here.
+template <typename T, uint32_t LPR, int U>
+__global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
+  constexpr int N = T::kVec;
+  constexpr uint32_t RPW = threads_of<LPR>() / LPR;
+  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
+  __shared__ float tile[RPW > 1 ? threads_of<LPR>() * U * N : 1];
+  const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  uint32_t turn = 0, at[U], skip[U];
+  float dw[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t c = (u * LPR + lane) * N;
+    at[u] = c < n.dim ? vec_at<T>(c, n.dim) : 0;
+    skip[u] = c < n.dim ? c - at[u] : N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[u][i] = 0.0f;
+  }
+  for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += (size_t)gridDim.x * RPW) {
+    const bool there = first + slot < n.ntokens;
+    const size_t t = there ? first + slot : n.ntokens - 1;
+    typename T::vec v[U], d[U], s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u] = d[u] = s[u] = zero_vec<T>();
+      if (skip[u] < N) {
+        v[u] = load_vec<T>(elem<T>(n.x, t * n.xstride + at[u]));
+        d[u] = load_vec<T>(elem<T>(n.dout, t * n.dstride + at[u]));
+        if (n.residual) s[u] = load_vec<T>(elem<T>(n.residual, t * n.rstride + at[u]));
+      }
+    }
+    float squares = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (skip[u] == N) continue;
+      float h[N], dy[N], w[N];
+      T::unpack(v[u], h);
+      T::unpack(d[u], dy);
+      load_weight<T>(n, at[u], w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float a = __builtin_fmaf(h[i], h[i], squares), b = __builtin_fmaf(dy[i] * w[i], h[i], dot);
+        squares = (uint32_t)i >= skip[u] ? a : squares;
+        dot = (uint32_t)i >= skip[u] ? b : dot;
+      }
+    }
+    join_row<LPR, Add, Add>(squares, dot, lds[turn]);
+    turn ^= 1;
+    const float r = inverse<LPR>(n, squares, [&] {
+      float sum = small_squares<T, U>(v, skip), none = 0.0f;
+      join_row<LPR, Add, Add>(sum, none, lds[turn]);
+      turn ^= 1;
+      return sum;
+    });
+    if (!there) continue;
+    const float back = dot / n.width * r * r;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (skip[u] == N) continue;
+      float h[N], dy[N], w[N], o[N];
+      T::unpack(v[u], h);
+      T::unpack(d[u], dy);
+      T::unpack(s[u], o);
+      load_weight<T>(n, at[u], w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dw[u][i] = __builtin_fmaf(dy[i] * r, h[i], dw[u][i]);
+        o[i] = __builtin_fmaf(r, __builtin_fmaf(-back, h[i], dy[i] * w[i]), o[i]);
+      }
+      store_vec<T>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(o));
+    }
+  }
+  if (!n.partials) return;
+  float* to = n.partials + (size_t)blockIdx.x * n.dim;
+  if constexpr (RPW == 1) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((uint32_t)i >= skip[u]) to[at[u] + i] = dw[u][i];
+    }
+  } else {
+    constexpr uint32_t wide = LPR * U * N;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((uint32_t)i >= skip[u]) tile[slot * wide + at[u] + i] = dw[u][i];
+    }
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < n.dim; c += threads_of<LPR>()) {
+      float sum = 0.0f;
+#pragma unroll
+      for (uint32_t k = 0; k < RPW; ++k) sum += tile[k * wide + c];
+      to[c] = sum;
+    }
+  }
+}
+
+// The columns' partials added up: 16 columns a workgroup, 16 lanes a column.
+template <typename D>
+__global__ void __launch_bounds__(kThreads) norm_dweight_kernel(const float* partials, uint32_t rows, uint32_t dim,
+                                                                void* dweight, int accumulate) {
+  __shared__ float tile[16][17];
+  const uint32_t c = blockIdx.x * 16 + threadIdx.x % 16, k = threadIdx.x / 16;
+  float sum = 0.0f;
+  if (c < dim)
+    for (uint32_t r = k; r < rows; r += 16) sum += partials[(size_t)r * dim + c];
+  tile[k][threadIdx.x % 16] = sum;
+  __syncthreads();
+  if (k == 0 && c < dim) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += tile[i][threadIdx.x];
+    typename D::raw* p = elem<D>(dweight, c);
+    *p = D::narrow(accumulate ? D::widen(*p) + sum : sum);
+  }
+}
+
+// fn(T{}, lanes per row, vectors per lane) for a type and a width.
+template <typename T, typename Fn>
+hipError_t with_width(size_t dim, Fn fn) {
+#define HC_ROW(L, U) fn(T{}, std::integral_constant<uint32_t, L>{}, std::integral_constant<int, U>{})
+  if constexpr (T::kVec == 1) {
+    return HC_ROW(8, 1);        // fewer columns than a vector has
+  } else {
+    const size_t vecs = (dim + T::kVec - 1) / T::kVec;
+    if (vecs <= 8) return HC_ROW(8, 1);
+    if (vecs <= 16) return HC_ROW(16, 1);
+    if (vecs <= 32) return HC_ROW(32, 1);
+    if (vecs <= 64) return HC_ROW(64, 1);
+    if (vecs <= 128) return HC_ROW(64, 2);
+    if (vecs <= 256) return HC_ROW(256, 1);
+    if (vecs <= 512) return HC_ROW(256, 2);
+    if (vecs <= 1024) return HC_ROW(256, 4);
+    if (vecs <= 2048) return HC_ROW(1024, 2);
+    if (vecs <= 4096) return HC_ROW(1024, 4);
+    if constexpr (T::kVec == 4) return HC_ROW(1024, 8);
+    return hipErrorInvalidValue;
+  }
+#undef HC_ROW
+}
+template <typename Fn>
+hipError_t with_row(hc_dtype_t dtype, size_t dim, Fn fn) {
+  if (dtype == HC_F32) return dim < F32::kVec ? with_width<F32S>(dim, fn) : with_width<F32>(dim, fn);
+  return dim < BF16::kVec ? with_width<BF16S>(dim, fn) : with_width<BF16>(dim, fn);
+}
+
+Norm norm_of(const NormRows& a) {
+  Norm n = {};
+  n.x = a.x;
+  n.xstride = a.xstride;
+  n.residual = a.residual;
+  n.rstride = a.rstride;
+  n.weight = a.weight;
+  n.wbf16 = a.wtype == HC_BF16;
+  n.sum = a.sum;
+  n.sstride = a.sstride;
+  n.out = a.out;
+  n.ostride = a.ostride;
+  n.ntokens = a.ntokens;
+  n.dim = (uint32_t)a.dim;
+  n.eps = a.eps;
+  n.width = (float)a.dim;
+  return n;
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormRows& a, bool q8, uint32_t group, float* scales, size_t cstride,
+                           hipStream_t stream) {
+  Norm n = norm_of(a);
+  n.scales = scales;
+  n.cstride = cstride;
+  n.groups = group ? (n.dim + group - 1) / group : 1;
+  n.group = n.groups > 1 ? group : 1u << 30;
+  return with_row(a.dtype, a.dim, [&](auto type, auto lanes, auto vecs) {
+    typedef decltype(type) T;
+    constexpr uint32_t LPR = decltype(lanes)::value, TH = threads_of<LPR>();
+    constexpr int U = decltype(vecs)::value;
+    const uint64_t groups = (n.ntokens + TH / LPR - 1) / (TH / LPR);
+    const uint32_t blocks = (uint32_t)(groups < kMaxBlocks ? groups : kMaxBlocks);
+    if (q8)
+      HC_ENQUEUE((norm_kernel<T, LPR, U, true>), blocks, TH, stream, n);
+    else
+      HC_ENQUEUE((norm_kernel<T, LPR, U, false>), blocks, TH, stream, n);
+    return hipSuccess;
+  });
+}
+
+size_t rms_norm_grad_ws_bytes(size_t ntokens, size_t dim) {
+  return (ntokens < kPartials ? ntokens : kPartials) * dim * sizeof(float);
+}
+
+hipError_t launch_rms_norm_grad(const NormRows& a, const void* dout, size_t dstride, void* dweight, hc_dtype_t dwtype,
+                                bool accumulate, void* ws, hipStream_t stream) {
+  Norm n = norm_of(a);
+  n.dout = dout;
+  n.dstride = dstride;
+  n.partials = dweight ? static_cast<float*>(ws) : nullptr;
+  uint32_t rows = 0;
+  if (n.ntokens) {
+    const hipError_t e = with_row(a.dtype, a.dim, [&](auto type, auto lanes, auto vecs) {
+      typedef decltype(type) T;
+      constexpr uint32_t LPR = decltype(lanes)::value, TH = threads_of<LPR>();
+      constexpr int U = decltype(vecs)::value;
+      const uint64_t groups = (n.ntokens + TH / LPR - 1) / (TH / LPR);
+      rows = (uint32_t)(groups < kPartials ? groups : kPartials);
+      HC_ENQUEUE((norm_grad_kernel<T, LPR, U>), rows, TH, stream, n);
+      return hipSuccess;
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!dweight) return hipSuccess;
+  const uint32_t blocks = (n.dim + 15) / 16;
+  if (dwtype == HC_F32)
+    HC_ENQUEUE(norm_dweight_kernel<F32>, blocks, kThreads, stream, n.partials, rows, n.dim, dweight, (int)accumulate);
+  else
+    HC_ENQUEUE(norm_dweight_kernel<BF16>, blocks, kThreads, stream, n.partials, rows, n.dim, dweight, (int)accumulate);
+  return hipSuccess;
+}
+
+}  // namespace hc

@@ -188,4 +188,19 @@ __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 63u; }
 // The wave's number in its workgroup, as a scalar.
 __device__ __forceinline__ uint32_t wave_id() { return first_lane_read(threadIdx.x >> 6); }
 
+// The tensor that holds chunk c, the last whose first chunk is not after it:
+// a search over 64 places at a time, one per lane, so two loads in turn find
+// it among 4096 tensors.  Every lane of the wave calls it.
+__device__ __forceinline__ uint32_t find_tensor(const uint32_t* first, uint32_t n, uint32_t c) {
+  uint32_t lo = 0;
+  while (n > 1) {
+    const uint32_t step = (n + 63) / 64, at = lane_id() * step;
+    const uint64_t not_after = __ballot(at < n && first[lo + at] <= c);
+    const uint32_t skip = ((uint32_t)__popcll(not_after) - 1) * step;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return first_lane_read(lo);
+}
+
 }  // namespace hc

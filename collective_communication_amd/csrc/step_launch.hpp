@@ -1,6 +1,7 @@
 // step_launch.hpp -- internal launch interface of the operators around the
 // gradient exchange: gradient norm and clipping, embedding lookup and
-// gradient, tokens sorted by expert and back.
+// gradient, the norm of rows, routing, tokens sorted by expert and back, and
+// the optimizer's step.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -75,5 +76,56 @@ hipError_t launch_expert_combine_grad(const void* dout, hc_dtype_t dtype, size_t
                                       const void* rows, size_t rstride, const hc_expert_plan_t& plan,
                                       const float* weights, void* drows, size_t drstride, float* dweights,
                                       hipStream_t stream);
+
+// ---- norm of rows (norm_kernels.hip)
+// Pointers with their strides; residual is the gradient that arrives at h, x is
+// h and out is dx for the gradient.
+struct NormRows {
+  const void* x;
+  size_t xstride;
+  const void* residual;
+  size_t rstride;
+  const void* weight;
+  hc_dtype_t wtype;
+  void* sum;
+  size_t sstride;
+  void* out;
+  size_t ostride;
+  hc_dtype_t dtype;
+  size_t ntokens, dim;
+  float eps;
+};
+// group: columns per scale, 0 for the whole row.
+hipError_t launch_rms_norm(const NormRows& a, bool q8, uint32_t group, float* scales, size_t cstride,
+                           hipStream_t stream);
+size_t rms_norm_grad_ws_bytes(size_t ntokens, size_t dim);
+hipError_t launch_rms_norm_grad(const NormRows& a, const void* dout, size_t dstride, void* dweight, hc_dtype_t dwtype,
+                                bool accumulate, void* ws, hipStream_t stream);
+
+// ---- routing (route_kernels.hip)
+hipError_t launch_route(const void* logits, hc_dtype_t dtype, size_t ntokens, uint32_t nexperts, size_t lstride,
+                        const hc_route_opts_t& o, int32_t* experts, float* weights, hipStream_t stream);
+hipError_t launch_route_grad(const void* logits, hc_dtype_t dtype, size_t ntokens, uint32_t nexperts, size_t lstride,
+                             const hc_route_opts_t& o, const int32_t* experts, const float* dweights, void* dlogits,
+                             size_t dstride, hipStream_t stream);
+
+// ---- AdamW (adamw_kernels.hip)
+struct AdamWTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;         // NULL: states of 32 bits
+  float* vs;
+  void* copy;
+  size_t count, index;
+  float decay;
+  hc_dtype_t p_dtype, g_dtype;
+};
+size_t adamw_table_bytes(size_t ntensors);
+// Writes the table and all of *plan but state_bits.
+hipError_t launch_adamw_plan(hc_adamw_plan_t* plan, const AdamWTensor* tensors, size_t n, void* table,
+                             hipStream_t stream);
+hipError_t launch_adamw(const hc_adamw_plan_t& plan, const hc_adamw_opts_t& o, hipStream_t stream);
 
 }  // namespace hc

@@ -2,7 +2,8 @@
  * hc.h -- C ABI of the MI355X (gfx950) emulated ring AllReduce data path and
  * the lossless bf16 exponent codecs, HCZ1 (fixed-length codes) and HCE1
  * (Huffman codes), and of the operators around the exchange: gradient norm and
- * clipping, embedding lookup and gradient, tokens by expert (library: libhc.so).
+ * clipping, embedding lookup and gradient, the norm of rows, routing to experts,
+ * tokens by expert, and the optimizer's step (library: libhc.so).
  *
  * The ring is emulated on ONE GPU: R "ranks" are R device buffers in the same
  * HBM; a hop's link transfer is the receiver reading the sender's buffer.  All
@@ -687,6 +688,192 @@ hc_status_t hc_expert_combine_grad(const void *dout, hc_dtype_t dtype, size_t di
                                    const void *rows, size_t rows_stride, const hc_expert_plan_t *plan,
                                    const float *weights, void *drows, size_t drows_stride, float *dweights,
                                    hipStream_t stream);
+
+/*
+ * The root-mean-square norm of rows, after a residual's addition:
+ *   h = round(x + residual)   (x itself where residual is NULL)
+ *   out = round(h * r * weight),   r = 1 / sqrt(mean of h^2 + eps)
+ * in fp32; h is rounded to the rows' type first, so that the norm and its
+ * gradient are of the values that sum_out holds.  No finite row's squares
+ * overflow.  A NaN makes its row NaN; an infinity makes the row 0 and itself NaN.
+ *   x, residual, sum_out, out: ntokens rows of dtype, each with its stride; dim
+ *     in 1..HC_MAX_NORM_DIM.
+ *     residual may be NULL, and so may sum_out (h is then not kept); sum_out
+ *     without residual is HC_ERR_INVALID_ARGUMENT.  sum_out and out may each
+ *     be x or residual, with its stride (not one the other).
+ *   weight: dim elements of weight_dtype.  eps >= 0, finite.
+ *
+ * hc_rms_norm_8bit writes rows of 8 bits (e4m3: 4 bits of exponent, 3 of
+ * mantissa, no infinities, largest 448), one byte each, with scales: for each
+ * group of `group` columns (32, 64, 128 or 256, the last one shorter; 0: the
+ * whole row)
+ *   t = h * weight,  a = largest |t| of the group,
+ *   out = nearest e4m3 of t * (448 / a),  scales[row][group] = a * r / 448,
+ * so that out * scale is the norm's output.  The codes do not depend on r, nor
+ * on any order of summation.  A group of zeroes has scale 0; one with a NaN or
+ * an infinity has a scale that is NaN.  A row of 8 bits with its scales may go
+ * through hc_expert_dispatch, two bytes as one bf16 element and a scale as fp32
+ * (the rows are copied as they are).
+ *   scales: ntokens rows of ceil(dim / group) (or 1) fp32, scales_stride apart.
+ */
+#define HC_MAX_NORM_DIM 32768
+hc_status_t hc_rms_norm(const void *x, hc_dtype_t dtype, size_t ntokens, size_t dim, size_t x_stride,
+                        const void *residual, size_t residual_stride, const void *weight,
+                        hc_dtype_t weight_dtype, float eps, void *sum_out, size_t sum_stride, void *out,
+                        size_t out_stride, hipStream_t stream);
+hc_status_t hc_rms_norm_8bit(const void *x, hc_dtype_t dtype, size_t ntokens, size_t dim, size_t x_stride,
+                             const void *residual, size_t residual_stride, const void *weight,
+                             hc_dtype_t weight_dtype, float eps, void *sum_out, size_t sum_stride, void *out,
+                             size_t out_stride, int group, float *scales, size_t scales_stride,
+                             hipStream_t stream);
+/*
+ * The gradient of hc_rms_norm, of its h (x there, or sum_out):
+ *   dx = round(r * (dout * weight - h * r^2 * mean(dout * weight * h)) + dsum)
+ *   dweight = round(sum over tokens of dout * h * r), or with accumulate != 0
+ *     round(dweight + that sum)
+ * in fp32; the order of the sums follows the sizes.
+ *   dsum: the gradient that arrives at h beside the norm's, or NULL.  dx may
+ *     be dout or dsum, with its stride.
+ *   dweight: dim elements of dweight_dtype, or NULL (not computed).
+ *   ws: hc_rms_norm_grad_workspace_bytes(ntokens, dim) bytes, which are enough
+ *     for fewer tokens and columns as well (0 on invalid sizes); none is needed
+ *     where dweight is NULL.
+ */
+size_t hc_rms_norm_grad_workspace_bytes(size_t ntokens, size_t dim);
+hc_status_t hc_rms_norm_grad(const void *dout, hc_dtype_t dtype, size_t ntokens, size_t dim, size_t dout_stride,
+                             const void *h, size_t h_stride, const void *weight, hc_dtype_t weight_dtype,
+                             float eps, const void *dsum, size_t dsum_stride, void *dx, size_t dx_stride,
+                             void *dweight, hc_dtype_t dweight_dtype, int accumulate, void *ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/*
+ * hc_route -- each token's k experts and their weights, from its logits:
+ *   s = softmax(logits) or sigmoid(logits), over or for each of nexperts;
+ *   c = s + bias (s itself without a bias);
+ *   of the ngroups groups of nexperts / ngroups experts in a row, the
+ *   top_groups with the largest value stay, the value being the largest c in
+ *   the group (group_best 1) or the sum of its two largest (2);
+ *   experts = the k largest c in them, the largest first;
+ *   weights = scale * s of each, divided by their sum if renormalise.
+ * Equal values go to the lowest group and expert.  The order is that of c (or,
+ * without a bias, of the logits) as 64 bits hold it; the weights are fp32.
+ * An expert whose logit or bias is -inf is never chosen, and adds nothing to
+ * its group's value; a slot that is left without one gets expert -1 and weight
+ * 0 (hc_expert_sort gives it no row).  A masked token is a row of -inf.  A NaN
+ * value comes before all others and makes its weights NaN (with softmax the
+ * whole row's).
+ *   logits: ntokens rows of nexperts elements of dtype, logits_stride apart.
+ *   bias: nexperts device fp32, or NULL: for balance; it moves the choice, not
+ *     the weights.
+ *   experts, weights: ntokens * k device int32 and fp32.
+ *   nexperts in 1..HC_MAX_EXPERTS, a multiple of ngroups; ngroups in
+ *   1..HC_MAX_GROUPS; top_groups in 1..ngroups; k in 1..HC_MAX_TOPK, at most
+ *   the experts of top_groups groups.
+ *
+ * hc_route_grad -- the gradient of the weights, the choice held:
+ *   dlogits = round(sum over j of dweights[j] * d weights[j] / d logits)
+ * for every expert, zero where nothing depends on it.  Slots whose expert is
+ * not in [0, nexperts), or has a logit of -inf, add nothing.  An expert that a
+ * token lists twice counts twice.  Of opts, k, scores, renormalise and scale
+ * are read.  dlogits may be logits, with its stride.
+ */
+typedef enum {
+    HC_SCORES_SOFTMAX = 0,
+    HC_SCORES_SIGMOID = 1,
+    HC_SCORES_RANGE_MIN_ = INT32_MIN,
+    HC_SCORES_RANGE_MAX_ = INT32_MAX
+} hc_scores_t;
+#define HC_MAX_GROUPS 64
+typedef struct {
+    int32_t k;
+    hc_scores_t scores;
+    int32_t ngroups;      /* 1: no groups */
+    int32_t top_groups;
+    int32_t group_best;   /* 1 or 2 */
+    int32_t renormalise;
+    float scale;
+    const float *bias;
+} hc_route_opts_t;
+hc_status_t hc_route(const void *logits, hc_dtype_t dtype, size_t ntokens, int nexperts, size_t logits_stride,
+                     const hc_route_opts_t *opts, int32_t *experts, float *weights, hipStream_t stream);
+hc_status_t hc_route_grad(const void *logits, hc_dtype_t dtype, size_t ntokens, int nexperts, size_t logits_stride,
+                          const hc_route_opts_t *opts, const int32_t *experts, const float *dweights,
+                          void *dlogits, size_t dlogits_stride, hipStream_t stream);
+
+/*
+ * An AdamW step over many tensors in one launch:
+ *   g' = c * g,  c = grad_scale * min(1, max_norm / (|grad_scale| * *d_norm + 1e-6))
+ *   m = beta1 * m + (1 - beta1) * g',  v = beta2 * v + (1 - beta2) * (g' * g')
+ *   p = p * (1 - lr * weight_decay * decay) -
+ *       lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32.  p is fp32 or bf16, g fp32 or bf16, whatever p is.
+ *
+ * hc_adamw_plan_t holds the tensors.  hc_adamw_plan writes their table into
+ * d_table (hc_adamw_table_bytes(ntensors) device bytes, 16-byte aligned) and
+ * fills in *plan (HOST); hc_adamw takes the step, as often as the tensors stay
+ * where they are.  The table must be written (stream order) before it is used.
+ *   params, grads, exp_avgs (m), exp_avg_sqs (v), counts, param_dtypes,
+ *     grad_dtypes: HOST arrays of ntensors entries, of which no host memory is
+ *     kept.  A tensor of count 0 is skipped.
+ *   State of 32 bits (m_scales and v_scales NULL): m and v are fp32.
+ *   m, v and what is stored of them are computed by the operations as they
+ *     stand here, each rounded once to fp32 (none fused), sqrt(v) and the
+ *     quotient by the scale among them: other programs can follow them bit for bit.
+ *   State of 8 bits: m holds e4m3 codes of m and v those of sqrt(v), a byte
+ *     each; m_scales[i] and v_scales[i] hold ceil(counts[i] / HC_STATE_BLOCK)
+ *     fp32, a scale for each block of HC_STATE_BLOCK values in a row:
+ *     value = code * scale, scale = largest magnitude of the block * (1 / 448) (0
+ *     for a block of zeroes, or of magnitudes below 2^-100).  The step's own p is computed
+ *     from m and v before they are rounded; a root that is not 0 is never
+ *     stored as 0.  Codes and scales of zero are the state before step 1.
+ *   copies: NULL, or an entry per tensor: NULL, or count bf16 values that
+ *     receive the updated fp32 parameter, rounded to nearest.
+ *   decays: NULL (all 1), or the factor of weight_decay per tensor.
+ *   What a plan writes must not overlap anything else in it: parameters, states,
+ *     scales and copies of all tensors (HC_ERR_INVALID_ARGUMENT).
+ *
+ * hc_adamw_opts_t:
+ *   step >= 1, or d_step, a device int64 that is read instead (a captured
+ *     launch then follows it); lr, or d_lr, a device fp32.
+ *   d_norm: device fp32, the norm of the gradients before grad_scale, to clip
+ *     by; NULL: no clipping, c = grad_scale.  max_norm >= 0.
+ *   skip_nonfinite: with d_norm, a norm that is infinite or NaN leaves
+ *     everything as it is.
+ *   seed: 0 rounds to nearest.  Else 8-bit states and bf16 parameters are
+ *     rounded up with the probability of what is cut off (to 1 / 65536), by 32
+ *     bits that are a function of seed, step, the tensor's place in the plan
+ *     and the value's in the tensor; small changes then count in the mean.
+ *       mix(x): x ^= x >> 16; x *= 0xB7E15163; x ^= x >> 15; x *= 0x6A09E667; x ^= x >> 16
+ *       key = mix(mix(mix(mix(low half of seed) ^ high half) ^ low half of step) ^ tensor)
+ *       bits = mix(mix(key ^ high half of i) + low half of i * 0x9E3779B9), mod 2^32
+ *     of which m takes the low 16, sqrt(v) the high 16, and p the high 16 of
+ *     bits * 0x9E3779B9, as (16 bits + 1/2) / 65536 for m and sqrt(v), and
+ *     added to the 16 bits that are cut off for p.
+ */
+#define HC_STATE_BLOCK 128
+typedef struct {
+    size_t ntensors;      /* that are not empty */
+    uint64_t chunks;
+    int32_t state_bits;
+    const void *d_table;
+} hc_adamw_plan_t;
+typedef struct {
+    int64_t step;
+    double lr, beta1, beta2, eps, weight_decay;
+    float grad_scale, max_norm;
+    const float *d_norm;
+    const float *d_lr;
+    const int64_t *d_step;
+    uint64_t seed;
+    int32_t skip_nonfinite;
+} hc_adamw_opts_t;
+size_t hc_adamw_table_bytes(size_t ntensors);
+hc_status_t hc_adamw_plan(hc_adamw_plan_t *plan, void *const *params, const void *const *grads,
+                          void *const *exp_avgs, void *const *exp_avg_sqs, float *const *m_scales,
+                          float *const *v_scales, void *const *copies, const float *decays, const size_t *counts,
+                          const hc_dtype_t *param_dtypes, const hc_dtype_t *grad_dtypes, size_t ntensors,
+                          void *d_table, size_t table_bytes, hipStream_t stream);
+hc_status_t hc_adamw(const hc_adamw_plan_t *plan, const hc_adamw_opts_t *opts, hipStream_t stream);
 
 const char *hc_status_string(hc_status_t status);
 const char *hc_last_error(void);  /* thread-local, "" when none */
