@@ -26,6 +26,7 @@
 // 12 tensors 5.4 us.  Non-temporal loads and stores: 2^25 values 162 us, 2^28 566.
 #include <math.h>
 
+#include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
 #include "step_launch.hpp"
@@ -243,14 +244,6 @@ __device__ __forceinline__ codes8 encode8(const float* f) {
   return v;
 }
 
-// The largest of 16 neighbouring lanes' values, in all of them.
-__device__ __forceinline__ uint32_t max16(uint32_t x) {
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));    // lane ^ 1
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));    // lane ^ 2
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));   // 7 - lane of 8
-  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // 15 - lane of 16
-}
-
 // x / unit rounded once, with inv = 1 / unit: the product's remainder corrects it.
 __device__ __forceinline__ float quotient(float x, float unit, float inv) {
   const float q = x * inv;
@@ -277,7 +270,7 @@ __device__ __forceinline__ codes8 quantise(const float* x, const uint32_t* bits,
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = max(top, ROOT ? f32_bits(x[j]) : f32_bits(x[j]) & 0x7FFFFFFFu);
-  const float a = bits_f32(max16(top));
+  const float a = bits_f32(join_lanes<16>(top, MaxOp{}));
   const bool tiny = a < kTinyBlock;
   const float unit = a * (1.0f / 448.0f), inv = tiny ? 0.0f : reciprocal(unit);
   *scale = tiny ? 0.0f : unit;

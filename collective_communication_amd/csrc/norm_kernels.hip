@@ -11,6 +11,7 @@
 // sums are joined there, and it is written from there.  The gradient of the
 // weight is summed over a workgroup's rows in registers and left as one row of
 // partials per workgroup, which a second launch adds in a fixed order.
+#include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
 #include "step_launch.hpp"
@@ -75,38 +76,37 @@ __device__ __forceinline__ void load_weight(const Norm& n, uint32_t c, float* w)
   }
 }
 
-struct Add {
-  static __device__ __forceinline__ float join(float a, float b) { return a + b; }
-};
-struct Max {
-  static __device__ __forceinline__ float join(float a, float b) { return a > b ? a : b; }
-};
-
-// v joined over `lanes` (a power of two, at most 64) neighbouring lanes.
-template <typename Op>
-__device__ __forceinline__ float join_lanes(float v, uint32_t lanes) {
-  for (uint32_t m = 1; m < lanes; m <<= 1) v = Op::join(v, __shfl_xor(v, (int)m));
-  return v;
+// The largest of `lanes` (4 to 64) neighbouring lanes' values.
+__device__ __forceinline__ float max_lanes(float v, uint32_t lanes) {
+  auto op = [](uint32_t a, uint32_t b) { return f32_bits(MaxOp{}(bits_f32(a), bits_f32(b))); };
+  uint32_t x = join_lanes<4>(f32_bits(v), op);
+  if (lanes > 4) x = join_step<4>(x, op);
+  if (lanes > 8) x = join_step<8>(x, op);
+  if (lanes > 16) x = join_step<16>(x, op);
+  if (lanes > 32) x = join_step<32>(x, op);
+  return bits_f32(x);
 }
+
 // Two values joined over the LPR lanes of a row, in all of them.  lds: a
 // workgroup's, another part for each call until a barrier.
 template <uint32_t LPR, typename A, typename B>
 __device__ __forceinline__ void join_row(float& a, float& b, float* lds) {
-  a = join_lanes<A>(a, LPR < 64 ? LPR : 64);
-  b = join_lanes<B>(b, LPR < 64 ? LPR : 64);
+  a = join_lanes<(LPR < 64 ? LPR : 64)>(a, A{});
+  b = join_lanes<(LPR < 64 ? LPR : 64)>(b, B{});
   if constexpr (LPR > 64) {
-    constexpr uint32_t W = LPR / 64;
+    constexpr uint32_t W = LPR / 64, ALL = threads_of<LPR>() / 64;
+    const uint32_t wave = threadIdx.x >> 6, from = wave / W * W;
     if (lane_id() == 0) {
-      lds[threadIdx.x >> 6] = a;
-      lds[W + (threadIdx.x >> 6)] = b;
+      lds[wave] = a;
+      lds[ALL + wave] = b;
     }
     __syncthreads();
-    a = lds[0];
-    b = lds[W];
+    a = lds[from];
+    b = lds[ALL + from];
 #pragma unroll
     for (uint32_t w = 1; w < W; ++w) {
-      a = A::join(a, lds[w]);
-      b = B::join(b, lds[W + w]);
+      a = A{}(a, lds[from + w]);
+      b = B{}(b, lds[ALL + from + w]);
     }
   }
 }
@@ -117,13 +117,14 @@ template <uint32_t LPR, typename Again>
 __device__ __forceinline__ float inverse(const Norm& n, float squares, Again again) {
   const bool past = squares == __builtin_inff();
   const float r = 1.0f / sqrtf(squares / n.width + n.eps);
-  if (!(LPR > 64 ? past : (bool)__any(past))) return r;
+  // a workgroup of several rows goes through the barrier together
+  if (!(LPR == threads_of<LPR>() ? past : LPR > 64 ? (bool)__syncthreads_or(past) : (bool)__any(past))) return r;
   const float small = again();
   return past ? 0x1p-80f / sqrtf(small / n.width + n.eps * 0x1p-80f * 0x1p-80f) : r;
 }
 
 // N e4m3 codes, nearest.
-template <int N>
+template <int N, bool NT>
 __device__ __forceinline__ void store_codes(uint8_t* p, const float* f, uint32_t skip) {
   if constexpr (N == 1) {
     *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[0], 0, false);
@@ -137,10 +138,16 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* f, uint32_t
     if (skip == 0) {
       if constexpr (N == 4) {
         typedef uint32_t word_u __attribute__((aligned(1)));
-        *reinterpret_cast<word_u*>(p) = w[0];
+        if constexpr (NT)
+          __builtin_nontemporal_store(w[0], reinterpret_cast<word_u*>(p));
+        else
+          *reinterpret_cast<word_u*>(p) = w[0];
       } else {
         typedef uint32_t vec2_u __attribute__((ext_vector_type(2), aligned(1)));
-        *reinterpret_cast<vec2_u*>(p) = vec2_u{w[0], w[1]};
+        if constexpr (NT)
+          __builtin_nontemporal_store(vec2_u{w[0], w[1]}, reinterpret_cast<vec2_u*>(p));
+        else
+          *reinterpret_cast<vec2_u*>(p) = vec2_u{w[0], w[1]};
       }
     } else {
 #pragma unroll
@@ -167,11 +174,11 @@ __device__ __forceinline__ float small_squares(const typename T::vec* v, const u
 }
 
 // Q8: rows of 8 bits.  LPR lanes have a row, U vectors each.
-template <typename T, uint32_t LPR, int U, bool Q8>
+template <typename T, uint32_t LPR, int U, bool Q8, bool NT>
 __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
   constexpr int N = T::kVec;
   constexpr uint32_t RPW = threads_of<LPR>() / LPR;
-  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
+  __shared__ float lds[2][LPR > 64 ? 2 * threads_of<LPR>() / 64 : 1];
   const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   uint32_t turn = 0;
   for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += (size_t)gridDim.x * RPW) {
@@ -185,13 +192,13 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       at[u] = c < n.dim ? vec_at<T>(c, n.dim) : 0;
       skip[u] = c < n.dim ? c - at[u] : N;                    // a vector moved back counts its own elements only
       v[u] = zero_vec<T>();
-      if (c < n.dim) v[u] = load_vec<T>(elem<T>(n.x, t * n.xstride + at[u]));
+      if (c < n.dim) v[u] = load_vec<T, NT>(elem<T>(n.x, t * n.xstride + at[u]));
     }
     if (n.residual) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         add[u] = zero_vec<T>();
-        if (skip[u] < N) add[u] = load_vec<T>(elem<T>(n.residual, t * n.rstride + at[u]));
+        if (skip[u] < N) add[u] = load_vec<T, NT>(elem<T>(n.residual, t * n.rstride + at[u]));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -221,30 +228,30 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
           load_weight<T>(n, at[u], w);
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            if ((uint32_t)i >= skip[u]) peak[u] = Max::join(fabsf(h[i] * w[i]), peak[u]);
+            if ((uint32_t)i >= skip[u]) peak[u] = MaxOp{}(fabsf(h[i] * w[i]), peak[u]);
         }
-        top = Max::join(peak[u], top);
+        top = MaxOp{}(peak[u], top);
       }
     }
-    join_row<LPR, Add, Max>(squares, top, lds[turn]);
+    join_row<LPR, SumOp, MaxOp>(squares, top, lds[turn]);
     turn ^= 1;
     const float r = inverse<LPR>(n, squares, [&] {
       float sum = small_squares<T, U>(v, skip), none = 0.0f;
-      join_row<LPR, Add, Add>(sum, none, lds[turn]);
+      join_row<LPR, SumOp, SumOp>(sum, none, lds[turn]);
       turn ^= 1;
       return sum;
     });
     if constexpr (Q8) {
       const uint32_t lanes = min(n.group / N, min(LPR, 64u));
 #pragma unroll
-      for (int u = 0; u < U; ++u) peak[u] = n.groups > 1 ? join_lanes<Max>(peak[u], lanes) : top;
+      for (int u = 0; u < U; ++u) peak[u] = n.groups > 1 ? max_lanes(peak[u], lanes) : top;
     }
     if (!there) continue;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (skip[u] == N) continue;
       float h[N], w[N];
-      if (n.sum) store_vec<T>(elem<T>(n.sum, t * n.sstride + at[u]), v[u]);
+      if (n.sum) store_vec<T, NT>(elem<T>(n.sum, t * n.sstride + at[u]), v[u]);
       T::unpack(v[u], h);
       load_weight<T>(n, at[u], w);
       if constexpr (Q8) {
@@ -253,13 +260,13 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
         const float inv = peak[u] > 0.0f ? 448.0f / (peak[u] * lift) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) h[i] = h[i] * w[i] * lift * inv;
-        store_codes<N>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
+        store_codes<N, NT>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
         const uint32_t c = at[u] + skip[u];
         if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = peak[u] * r / 448.0f;
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) h[i] = h[i] * r * w[i];
-        store_vec<T>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(h));
+        store_vec<T, NT>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(h));
       }
     }
   }
@@ -270,7 +277,7 @@ template <typename T, uint32_t LPR, int U>
 __global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
   constexpr int N = T::kVec;
   constexpr uint32_t RPW = threads_of<LPR>() / LPR;
-  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
+  __shared__ float lds[2][LPR > 64 ? 2 * threads_of<LPR>() / 64 : 1];
   __shared__ float tile[RPW > 1 ? threads_of<LPR>() * U * N : 1];
   const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   uint32_t turn = 0, at[U], skip[U];
@@ -311,11 +318,11 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
         dot = (uint32_t)i >= skip[u] ? b : dot;
       }
     }
-    join_row<LPR, Add, Add>(squares, dot, lds[turn]);
+    join_row<LPR, SumOp, SumOp>(squares, dot, lds[turn]);
     turn ^= 1;
     const float r = inverse<LPR>(n, squares, [&] {
       float sum = small_squares<T, U>(v, skip), none = 0.0f;
-      join_row<LPR, Add, Add>(sum, none, lds[turn]);
+      join_row<LPR, SumOp, SumOp>(sum, none, lds[turn]);
       turn ^= 1;
       return sum;
     });
@@ -441,17 +448,20 @@ hipError_t launch_rms_norm(const NormRows& a, bool q8, uint32_t group, float* sc
   n.cstride = cstride;
   n.groups = group ? (n.dim + group - 1) / group : 1;
   n.group = n.groups > 1 ? group : 1u << 30;
+  const size_t es = a.dtype == HC_F32 ? 4 : 2, bytes = n.ntokens * n.dim * ((q8 ? 1 : es) + (n.sum ? es : 0));
+  const bool nt = bytes >= kStreamStoreBytes;     // what is read is as much at least
   return with_row(a.dtype, a.dim, [&](auto type, auto lanes, auto vecs) {
     typedef decltype(type) T;
     constexpr uint32_t LPR = decltype(lanes)::value, TH = threads_of<LPR>();
     constexpr int U = decltype(vecs)::value;
     const uint64_t groups = (n.ntokens + TH / LPR - 1) / (TH / LPR);
     const uint32_t blocks = (uint32_t)(groups < kMaxBlocks ? groups : kMaxBlocks);
-    if (q8)
-      HC_ENQUEUE((norm_kernel<T, LPR, U, true>), blocks, TH, stream, n);
-    else
-      HC_ENQUEUE((norm_kernel<T, LPR, U, false>), blocks, TH, stream, n);
-    return hipSuccess;
+    auto launch = [&](auto kernel) {
+      HC_ENQUEUE(kernel, blocks, TH, stream, n);
+      return hipSuccess;
+    };
+    if (q8) return nt ? launch(norm_kernel<T, LPR, U, true, true>) : launch(norm_kernel<T, LPR, U, true, false>);
+    return nt ? launch(norm_kernel<T, LPR, U, false, true>) : launch(norm_kernel<T, LPR, U, false, false>);
   });
 }
 

@@ -16,6 +16,7 @@
 // 128: 4.4 us.
 #include <type_traits>
 
+#include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
 #include "step_launch.hpp"
@@ -41,34 +42,18 @@ struct Route {
   float scale;
 };
 
-// v joined over a token's LPT lanes, in all of them.
-template <uint32_t LPT, typename Op>
-__device__ __forceinline__ uint32_t join_token(uint32_t v, Op op) {
-  if constexpr (LPT > 1) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
-  if constexpr (LPT > 2) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
-  if constexpr (LPT > 4) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
-  if constexpr (LPT > 8) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
-  if constexpr (LPT > 16) {
-    const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = op((uint32_t)x[0], (uint32_t)x[1]);
-  }
-  if constexpr (LPT > 32) {
-    const auto x = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    v = op((uint32_t)x[0], (uint32_t)x[1]);
-  }
-  return v;
-}
+// Joined over a token's LPT lanes, in all of them.
 template <uint32_t LPT>
 __device__ __forceinline__ uint32_t max_token(uint32_t v) {
-  return join_token<LPT>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  return join_lanes<LPT>(v, MaxOp{});
 }
 template <uint32_t LPT>
 __device__ __forceinline__ float max_token(float v) {
-  return bits_f32(join_token<LPT>(f32_bits(v), [](uint32_t a, uint32_t b) { return f32_bits(fmaxf(bits_f32(a), bits_f32(b))); }));
+  return join_lanes<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <uint32_t LPT>
 __device__ __forceinline__ float sum_token(float v) {
-  return bits_f32(join_token<LPT>(f32_bits(v), [](uint32_t a, uint32_t b) { return f32_bits(bits_f32(a) + bits_f32(b)); }));
+  return join_lanes<LPT>(v, SumOp{});
 }
 
 // fp64 words that order as their values: NaN after all, 0 for what is never chosen.
