@@ -26,6 +26,7 @@
 // 12 tensors 5.4 us.  Non-temporal loads and stores: 2^25 values 162 us, 2^28 566.
 #include <math.h>
 
+#include "arith.hpp"
 #include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
@@ -242,23 +243,6 @@ __device__ __forceinline__ codes8 encode8(const float* f) {
     v[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j + 2], f[4 * j + 3], w, true);
   }
   return v;
-}
-
-// x / unit rounded once, with inv = 1 / unit: the product's remainder corrects it.
-__device__ __forceinline__ float quotient(float x, float unit, float inv) {
-  const float q = x * inv;
-  return __builtin_fmaf(__builtin_fmaf(-q, unit, x), inv, q);
-}
-// 1 / x and sqrt(x) rounded once for normal x, from the 1-ulp instructions and
-// one step of Newton's method (as the full division and root on all 2^24
-// mantissas of two octaves).  A subnormal root is near.
-__device__ __forceinline__ float reciprocal(float x) {
-  const float r = __builtin_amdgcn_rcpf(x);
-  return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
-}
-__device__ __forceinline__ float root_of(float x) {
-  const float r = __builtin_amdgcn_rsqf(__builtin_fmaxf(x, 0x1p-126f)), s = x * r;
-  return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * r, s);
 }
 
 // Eight values of each of 16 lanes, as codes and the block's scale.  A NaN or an

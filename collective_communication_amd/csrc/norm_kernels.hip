@@ -7,10 +7,22 @@
 //   dx = round(r (dy w - h r^2 mean(dy w h)) + dsum),  dw = sum over rows of dy h r
 //
 // All are streams over rows: a row is loaded once into the registers of as many
-// lanes as its width has vectors for (8 to 64 of a wave, or 4 or 16 waves), its
+// lanes as its width has vectors for (8 to 64 of a wave, or 4, 8 or 16 waves), its
 // sums are joined there, and it is written from there.  The gradient of the
 // weight is summed over a workgroup's rows in registers and left as one row of
 // partials per workgroup, which a second launch adds in a fixed order.
+//
+// Measured (a large copy reaches 4.8-5.2 TB/s here): 16,384 x 4096 bf16 with a residual
+// to 8 bits, a scale for 128 columns (472 MB) 91 us, 5.2 TB/s (105 with plain
+// stores and joins through shared memory, 111 by 8 waves a row, 126 by 2); 60,000 x
+// 2048 without a residual, which is bound by the lanes' work, 110 us (131 with full
+// divisions and each product made twice).  Its gradient with dsum, 16,384 x
+// 4096 (537 MB) 97 us, 5.5 TB/s, and 7 for the weight's partials: 118 without the
+// next row's loads ahead, or with them and 130 registers instead of 128.
+// 64 x 4096 to 8 bits 4.5 us, 500 x 2560 fp32 gradient 6.8 + 6.1.
+#include <type_traits>
+
+#include "arith.hpp"
 #include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
@@ -20,7 +32,7 @@ namespace hc {
 namespace {
 
 constexpr uint32_t kMaxBlocks = 1u << 22;
-constexpr uint32_t kPartials = 1024;         // workgroups that leave a row of partial sums
+constexpr uint32_t kPartials = 1024;         // workgroups of 4 waves that leave a row of partial sums
 
 struct Norm {
   const void* x;
@@ -40,7 +52,7 @@ struct Norm {
   size_t ntokens;
   uint32_t dim, group, groups;   // group: columns, the row's width or more for one
   uint32_t wbf16;
-  float eps, width;          // the row's width
+  float eps, width, per_width;   // the row's width and 1 / it
 };
 
 template <uint32_t LPR>
@@ -111,16 +123,21 @@ __device__ __forceinline__ void join_row(float& a, float& b, float* lds) {
   }
 }
 
+// 1 / sqrt(x), also of subnormal x.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool small = x < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(small ? x * 0x1p64f : x) * (small ? 0x1p32f : 1.0f);
+}
 // 1 / sqrt(mean of squares + eps).  Where the squares pass what fp32 holds they
 // are summed once more, of values 2^80 smaller: again() does.
 template <uint32_t LPR, typename Again>
 __device__ __forceinline__ float inverse(const Norm& n, float squares, Again again) {
   const bool past = squares == __builtin_inff();
-  const float r = 1.0f / sqrtf(squares / n.width + n.eps);
+  const float r = inverse_root((past ? squares : quotient(squares, n.width, n.per_width)) + n.eps);
   // a workgroup of several rows goes through the barrier together
   if (!(LPR == threads_of<LPR>() ? past : LPR > 64 ? (bool)__syncthreads_or(past) : (bool)__any(past))) return r;
-  const float small = again();
-  return past ? 0x1p-80f / sqrtf(small / n.width + n.eps * 0x1p-80f * 0x1p-80f) : r;
+  const float small = again() * n.per_width;      // an infinity's stay one
+  return past ? 0x1p-80f * inverse_root(small + n.eps * 0x1p-80f * 0x1p-80f) : r;
 }
 
 // N e4m3 codes, nearest.
@@ -211,7 +228,7 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       }
     }
     float squares = 0.0f, top = 0.0f;
-    float peak[U];
+    float peak[U], prod[Q8 ? U : 1][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float h[N];
@@ -227,8 +244,10 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
           float w[N];
           load_weight<T>(n, at[u], w);
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if ((uint32_t)i >= skip[u]) peak[u] = MaxOp{}(fabsf(h[i] * w[i]), peak[u]);
+          for (int i = 0; i < N; ++i) {
+            prod[u][i] = h[i] * w[i];
+            if ((uint32_t)i >= skip[u]) peak[u] = MaxOp{}(fabsf(prod[u][i]), peak[u]);
+          }
         }
         top = MaxOp{}(peak[u], top);
       }
@@ -252,18 +271,18 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       if (skip[u] == N) continue;
       float h[N], w[N];
       if (n.sum) store_vec<T, NT>(elem<T>(n.sum, t * n.sstride + at[u]), v[u]);
-      T::unpack(v[u], h);
-      load_weight<T>(n, at[u], w);
       if constexpr (Q8) {
         // a group of tiny values is brought up first, so that 448 / a stays finite
-        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : 1.0f;
-        const float inv = peak[u] > 0.0f ? 448.0f / (peak[u] * lift) : 0.0f;
+        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : 1.0f, a = peak[u] * lift;
+        const float inv = peak[u] > 0.0f ? quotient(448.0f, a, reciprocal(a)) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) h[i] = h[i] * w[i] * lift * inv;
+        for (int i = 0; i < N; ++i) h[i] = prod[u][i] * lift * inv;
         store_codes<N, NT>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
         const uint32_t c = at[u] + skip[u];
-        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = peak[u] * r / 448.0f;
+        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = peak[u] * (r * (1.0f / 448.0f));
       } else {
+        T::unpack(v[u], h);
+        load_weight<T>(n, at[u], w);
 #pragma unroll
         for (int i = 0; i < N; ++i) h[i] = h[i] * r * w[i];
         store_vec<T, NT>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(h));
@@ -272,16 +291,18 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
   }
 }
 
-// x is h here.
-template <typename T, uint32_t LPR, int U>
-__global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
+// x is h here.  A row's loads are on their way while the row before it is
+// summed and written, and the weights stay in registers where there is room.
+template <typename T, uint32_t LPR, int U, bool NT>
+__global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && U * T::kVec == 16 ? 4 : 1) norm_grad_kernel(Norm n) {
   constexpr int N = T::kVec;
   constexpr uint32_t RPW = threads_of<LPR>() / LPR;
+  constexpr bool kAhead = U * N <= 16 && LPR < 1024;
   __shared__ float lds[2][LPR > 64 ? 2 * threads_of<LPR>() / 64 : 1];
   __shared__ float tile[RPW > 1 ? threads_of<LPR>() * U * N : 1];
   const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   uint32_t turn = 0, at[U], skip[U];
-  float dw[U][N];
+  float dw[U][N], wk[kAhead ? U : 1][N];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t c = (u * LPR + lane) * N;
@@ -289,30 +310,46 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
     skip[u] = c < n.dim ? c - at[u] : N;
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[u][i] = 0.0f;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) wk[u][i] = 0.0f;
+      if (skip[u] < N) load_weight<T>(n, at[u], wk[u]);
+    }
   }
-  for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += (size_t)gridDim.x * RPW) {
-    const bool there = first + slot < n.ntokens;
-    const size_t t = there ? first + slot : n.ntokens - 1;
+  struct Row {
     typename T::vec v[U], d[U], s[U];
+  };
+  auto load = [&](size_t first, Row& r) {
+    const size_t t = first + slot < n.ntokens ? first + slot : n.ntokens - 1;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      v[u] = d[u] = s[u] = zero_vec<T>();
+      r.v[u] = r.d[u] = r.s[u] = zero_vec<T>();
       if (skip[u] < N) {
-        v[u] = load_vec<T>(elem<T>(n.x, t * n.xstride + at[u]));
-        d[u] = load_vec<T>(elem<T>(n.dout, t * n.dstride + at[u]));
-        if (n.residual) s[u] = load_vec<T>(elem<T>(n.residual, t * n.rstride + at[u]));
+        r.v[u] = load_vec<T, NT>(elem<T>(n.x, t * n.xstride + at[u]));
+        r.d[u] = load_vec<T, NT>(elem<T>(n.dout, t * n.dstride + at[u]));
+        if (kAhead && n.residual) r.s[u] = load_vec<T, NT>(elem<T>(n.residual, t * n.rstride + at[u]));
       }
     }
+  };
+  Row row, next;
+  const size_t step = (size_t)gridDim.x * RPW;
+  load((size_t)blockIdx.x * RPW, row);
+  for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += step) {
+    const size_t t = first + slot;
+    const bool there = t < n.ntokens, more = first + step < n.ntokens;
+    if constexpr (kAhead)
+      if (more) load(first + step, next);
     float squares = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (skip[u] == N) continue;
       float h[N], dy[N], w[N];
-      T::unpack(v[u], h);
-      T::unpack(d[u], dy);
-      load_weight<T>(n, at[u], w);
+      T::unpack(row.v[u], h);
+      T::unpack(row.d[u], dy);
+      if constexpr (!kAhead) load_weight<T>(n, at[u], w);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        if constexpr (kAhead) w[i] = wk[u][i];
         const float a = __builtin_fmaf(h[i], h[i], squares), b = __builtin_fmaf(dy[i] * w[i], h[i], dot);
         squares = (uint32_t)i >= skip[u] ? a : squares;
         dot = (uint32_t)i >= skip[u] ? b : dot;
@@ -321,28 +358,38 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
     join_row<LPR, SumOp, SumOp>(squares, dot, lds[turn]);
     turn ^= 1;
     const float r = inverse<LPR>(n, squares, [&] {
-      float sum = small_squares<T, U>(v, skip), none = 0.0f;
+      float sum = small_squares<T, U>(row.v, skip), none = 0.0f;
       join_row<LPR, SumOp, SumOp>(sum, none, lds[turn]);
       turn ^= 1;
       return sum;
     });
-    if (!there) continue;
-    const float back = dot / n.width * r * r;
+    if (there) {
+      const float back = dot * n.per_width * r * r;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (skip[u] == N) continue;
-      float h[N], dy[N], w[N], o[N];
-      T::unpack(v[u], h);
-      T::unpack(d[u], dy);
-      T::unpack(s[u], o);
-      load_weight<T>(n, at[u], w);
+      for (int u = 0; u < U; ++u) {
+        if (skip[u] == N) continue;
+        float h[N], dy[N], w[N], o[N];
+        T::unpack(row.v[u], h);
+        T::unpack(row.d[u], dy);
+        if constexpr (!kAhead) {
+          load_weight<T>(n, at[u], w);
+          if (n.residual) row.s[u] = load_vec<T, NT>(elem<T>(n.residual, t * n.rstride + at[u]));
+        }
+        T::unpack(row.s[u], o);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        dw[u][i] = __builtin_fmaf(dy[i] * r, h[i], dw[u][i]);
-        o[i] = __builtin_fmaf(r, __builtin_fmaf(-back, h[i], dy[i] * w[i]), o[i]);
+        for (int i = 0; i < N; ++i) {
+          if constexpr (kAhead) w[i] = wk[u][i];
+          dw[u][i] = __builtin_fmaf(dy[i] * r, h[i], dw[u][i]);
+          o[i] = __builtin_fmaf(r, __builtin_fmaf(-back, h[i], dy[i] * w[i]), o[i]);
+        }
+        store_vec<T, NT>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(o));
       }
-      store_vec<T>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(o));
     }
+    if (!more) break;
+    if constexpr (kAhead)
+      row = next;
+    else
+      load(first + step, row);
   }
   if (!n.partials) return;
   float* to = n.partials + (size_t)blockIdx.x * n.dim;
@@ -371,23 +418,44 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_grad_kernel(Norm n) {
   }
 }
 
-// The columns' partials added up: 16 columns a workgroup, 16 lanes a column.
-template <typename D>
+// The columns' partials added up: 16 columns a workgroup, by V (4, or 1 for
+// fewer columns) in each of 64 (16) lanes that share a column's rows.
+template <typename V, typename D>
 __global__ void __launch_bounds__(kThreads) norm_dweight_kernel(const float* partials, uint32_t rows, uint32_t dim,
                                                                 void* dweight, int accumulate) {
-  __shared__ float tile[16][17];
-  const uint32_t c = blockIdx.x * 16 + threadIdx.x % 16, k = threadIdx.x / 16;
-  float sum = 0.0f;
-  if (c < dim)
-    for (uint32_t r = k; r < rows; r += 16) sum += partials[(size_t)r * dim + c];
-  tile[k][threadIdx.x % 16] = sum;
-  __syncthreads();
-  if (k == 0 && c < dim) {
-    sum = 0.0f;
+  constexpr uint32_t N = V::kVec, kLanes = 16 / N, kRows = kThreads / kLanes;
+  __shared__ float tile[kWaves][16];
+  const uint32_t c = blockIdx.x * 16 + threadIdx.x % kLanes * N, k = threadIdx.x / kLanes;
+  const uint32_t at = c < dim ? vec_at<V>(c, dim) : 0;
+  float sum[N];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += tile[i][threadIdx.x];
-    typename D::raw* p = elem<D>(dweight, c);
-    *p = D::narrow(accumulate ? D::widen(*p) + sum : sum);
+  for (uint32_t i = 0; i < N; ++i) sum[i] = 0.0f;
+  if (c < dim) {
+#pragma unroll 8
+    for (uint32_t r = k; r < rows; r += kRows) {
+      float f[N];
+      V::unpack(load_vec<V>(elem<V>(partials, (size_t)r * dim + at)), f);
+#pragma unroll
+      for (uint32_t i = 0; i < N; ++i) sum[i] += f[i];
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < N; ++i) {
+#pragma unroll
+    for (uint32_t m = kLanes; m < 64; m <<= 1) sum[i] += __shfl_xor(sum[i], (int)m);
+    if (lane_id() < kLanes) tile[threadIdx.x >> 6][threadIdx.x % kLanes * N + i] = sum[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kLanes && c < dim) {
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+      if (at + i < c) continue;        // of the vector before
+      float total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total += tile[w][threadIdx.x * N + i];
+      typename D::raw* p = elem<D>(dweight, at + i);
+      *p = D::narrow(accumulate ? D::widen(*p) + total : total);
+    }
   }
 }
 
@@ -406,7 +474,7 @@ hipError_t with_width(size_t dim, Fn fn) {
     if (vecs <= 128) return HC_ROW(64, 2);
     if (vecs <= 256) return HC_ROW(256, 1);
     if (vecs <= 512) return HC_ROW(256, 2);
-    if (vecs <= 1024) return HC_ROW(256, 4);
+    if (vecs <= 1024) return HC_ROW(512, 2);
     if (vecs <= 2048) return HC_ROW(1024, 2);
     if (vecs <= 4096) return HC_ROW(1024, 4);
     if constexpr (T::kVec == 4) return HC_ROW(1024, 8);
@@ -436,6 +504,7 @@ Norm norm_of(const NormRows& a) {
   n.dim = (uint32_t)a.dim;
   n.eps = a.eps;
   n.width = (float)a.dim;
+  n.per_width = 1.0f / n.width;
   return n;
 }
 
@@ -482,19 +551,26 @@ hipError_t launch_rms_norm_grad(const NormRows& a, const void* dout, size_t dstr
       constexpr uint32_t LPR = decltype(lanes)::value, TH = threads_of<LPR>();
       constexpr int U = decltype(vecs)::value;
       const uint64_t groups = (n.ntokens + TH / LPR - 1) / (TH / LPR);
-      rows = (uint32_t)(groups < kPartials ? groups : kPartials);
-      HC_ENQUEUE((norm_grad_kernel<T, LPR, U>), rows, TH, stream, n);
+      constexpr uint32_t most = kPartials * kThreads / TH;     // as many waves, and fewer partials of wider rows
+      rows = (uint32_t)(groups < most ? groups : most);
+      // rows read once, which the step before has mostly left in memory from here on
+      if (n.ntokens * n.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
+        HC_ENQUEUE((norm_grad_kernel<T, LPR, U, true>), rows, TH, stream, n);
+      else
+        HC_ENQUEUE((norm_grad_kernel<T, LPR, U, false>), rows, TH, stream, n);
       return hipSuccess;
     });
     if (e != hipSuccess) return e;
   }
   if (!dweight) return hipSuccess;
   const uint32_t blocks = (n.dim + 15) / 16;
-  if (dwtype == HC_F32)
-    HC_ENQUEUE(norm_dweight_kernel<F32>, blocks, kThreads, stream, n.partials, rows, n.dim, dweight, (int)accumulate);
-  else
-    HC_ENQUEUE(norm_dweight_kernel<BF16>, blocks, kThreads, stream, n.partials, rows, n.dim, dweight, (int)accumulate);
-  return hipSuccess;
+  auto launch = [&](auto kernel) {
+    HC_ENQUEUE(kernel, blocks, kThreads, stream, n.partials, rows, n.dim, dweight, (int)accumulate);
+    return hipSuccess;
+  };
+  if (n.dim < F32::kVec)
+    return dwtype == HC_F32 ? launch(norm_dweight_kernel<F32S, F32>) : launch(norm_dweight_kernel<F32S, BF16>);
+  return dwtype == HC_F32 ? launch(norm_dweight_kernel<F32, F32>) : launch(norm_dweight_kernel<F32, BF16>);
 }
 
 }  // namespace hc
