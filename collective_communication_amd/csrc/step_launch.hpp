@@ -15,16 +15,22 @@ namespace hc {
 // Enqueues a kernel and returns that launch's own status: not whatever error
 // an earlier call of the process may have left behind.  The arguments are
 // converted to the kernel's parameter types.
+// lds: bytes of shared memory beside the kernel's own.
 template <typename... P, typename... A>
-inline hipError_t enqueue(void (*kernel)(P...), uint32_t grid, uint32_t block, hipStream_t stream, const A&... args) {
+inline hipError_t enqueue_lds(uint32_t lds, void (*kernel)(P...), uint32_t grid, uint32_t block, hipStream_t stream,
+                              const A&... args) {
   static_assert(sizeof...(P) == sizeof...(A), "one argument per parameter");
   return [&](const P&... p) {
     const void* at[] = {static_cast<const void*>(&p)...};
     const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(block),
-                                         const_cast<void**>(at), 0, stream);
+                                         const_cast<void**>(at), lds, stream);
     if (e != hipSuccess) (void)hipGetLastError();   // reported here, so not once more by the next reader
     return e;
   }(args...);
+}
+template <typename... P, typename... A>
+inline hipError_t enqueue(void (*kernel)(P...), uint32_t grid, uint32_t block, hipStream_t stream, const A&... args) {
+  return enqueue_lds(0, kernel, grid, block, stream, args...);
 }
 #define HC_ENQUEUE(kernel, ...) \
   do { \
