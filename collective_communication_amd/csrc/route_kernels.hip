@@ -586,15 +586,23 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(Route r) {
     if (id[j] < 0) continue;
     const float v = raw[j], a = raw_weight(r, v, top, z, xm);
     sum += a;
-    dot = __builtin_fmaf(a, val[j], dot);
-    raw[j] = r.sigmoid ? a / (1.0f + expf(v)) : a;      // 1 - sigmoid(v) beside it
+    raw[j] = a;
   }
-  sum = sum_token<LPT>(sum);
+  if (r.renormalise) sum = sum_token<LPT>(sum);
+  // shares first, so that a single one is 1 and its gradient 0
+  for (uint32_t j = lane; j < r.k; j += LPT) {
+    if (id[j] < 0) continue;
+    if (r.renormalise) raw[j] /= sum;
+    dot = __builtin_fmaf(raw[j], val[j], dot);
+  }
   dot = sum_token<LPT>(dot);
-  // d/dx of each slot
-  const float mean = r.renormalise ? dot / sum : 0.0f, per = r.renormalise ? 1.0f / sum : 1.0f;
-  for (uint32_t j = lane; j < r.k; j += LPT)
-    if (id[j] >= 0) val[j] = raw[j] * per * (val[j] - mean);
+  // d/dx of each slot, with 1 - sigmoid(x)
+  for (uint32_t j = lane; j < r.k; j += LPT) {
+    const int32_t e = id[j];
+    if (e < 0) continue;
+    const float d = raw[j] * (r.renormalise ? val[j] - dot : val[j]);
+    val[j] = r.sigmoid ? d / (1.0f + expf(T::widen(x[e]))) : d;
+  }
   if (dense) {
     const float share = z == 0.0f ? 0.0f : -dot / z;
     for (uint32_t e = lane; e < r.nexperts; e += LPT) row[e] *= share;

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from collective_communication_amd import binding as hc
-from test_gpu_step_ops import B, F, HALF, TINY, U, check_guards, close, gen, guarded
+from test_gpu_step_ops import B, F, GUARD, HALF, TINY, U, check_guards, close, gen, guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -230,6 +230,19 @@ def test_gradient(n, k, scores, renormalise):
                            if renormalise else 1.0) * s * (k + 8) * 2.0 ** -53
             close(dx, want, each * 2 * (130 + k) * U + left + want.abs() * HALF[dtype] + TINY[dtype], f"{t} x {n}")
             check_guards(buf, dx)
+
+
+def test_gradient_of_a_single_choice():
+    """One renormalised weight is its scale, whatever the logits: no gradient at
+    all, not even a rounding's."""
+    g = gen(25)
+    x, dw = logits(g, 500, 87, B, spread=3.0), torch.randn((500, 1), generator=g, device="cuda")
+    for scores in ("softmax", "sigmoid"):
+        e, w = route(x, 1, scores=scores, scale=2.5)
+        assert bool((w == 2.5).all())
+        dx = torch.full_like(x, GUARD)
+        hc.hc_route_grad(x, e, dw, dx, scores=scores, scale=2.5)
+        assert bool((dx == 0).all())
 
 
 def test_gradient_against_differences():
