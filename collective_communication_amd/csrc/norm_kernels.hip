@@ -31,7 +31,7 @@
 namespace hc {
 namespace {
 
-constexpr uint32_t kMaxBlocks = 1u << 22;
+constexpr uint32_t kMaxBlocks = 1u << 21;    // of up to 1024 lanes: they are counted in 32 bits
 constexpr uint32_t kPartials = 1024;         // workgroups of 4 waves that leave a row of partial sums
 
 struct Norm {

@@ -25,7 +25,6 @@ namespace hc {
 namespace {
 
 constexpr uint32_t kMaxBlocks = 1u << 22;
-constexpr uint32_t kMaxExperts = HC_MAX_EXPERTS;
 
 struct Route {
   const void* logits;
@@ -239,6 +238,8 @@ __device__ __forceinline__ float value32(uint32_t o) {
   return bits_f32(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
 }
 
+constexpr uint32_t kMore = 8;             // candidates past the k-th
+
 // A token by LPT neighbouring lanes, V experts in a row each (a group by
 // group_lanes of them), as 32-bit keys: the choice value's upper bits and, in
 // the lowest, which of the lane's it is, so that a lane's largest is found by
@@ -249,13 +250,13 @@ __device__ __forceinline__ float value32(uint32_t o) {
 template <typename T, uint32_t LPT, uint32_t V>
 __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel(Route r) {
   constexpr uint32_t N = T::kVec < V ? T::kVec : V, kTokens = kThreads / LPT;
-  constexpr uint32_t kMore = 8;             // candidates past the k-th
-  __shared__ uint32_t slot_id[kTokens][HC_MAX_TOPK + kMore], slot_key[kTokens][HC_MAX_TOPK + kMore];
-  __shared__ float slot_x[kTokens][HC_MAX_TOPK];
-  __shared__ uint64_t keys64[kWaves][LPT * V < kMaxExperts ? LPT * V : kMaxExperts];
+  extern __shared__ __align__(16) uint64_t shared64[];      // as launch_route sizes it
+  uint64_t* keys64 = shared64 + wave_id() * r.nexperts;
+  uint32_t* slots = reinterpret_cast<uint32_t*>(shared64 + kWaves * r.nexperts);
   const uint32_t wave = wave_id(), lane = lane_id() % LPT, seg = lane_id() - lane, slot = threadIdx.x / LPT;
-  uint32_t *ids = slot_id[slot], *keep = slot_key[slot];
-  float* chosen_x = slot_x[slot];
+  const uint32_t room = r.k + kMore;
+  uint32_t *ids = slots + slot * 2 * room, *keep = ids + room;
+  float* chosen_x = reinterpret_cast<float*>(slots + kTokens * 2 * room) + slot * r.k;
   const uint32_t g = lane / r.group_lanes, in_group = lane % r.group_lanes;
   const uint32_t n = g < r.groups && in_group * V < r.group_size ? min(V, r.group_size - in_group * V) : 0;
   const uint32_t e0 = n ? g * r.group_size + in_group * V : 0;
@@ -520,9 +521,9 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
     const uint32_t at = (uint32_t)__builtin_ctzll(redo) / LPT;         // which of the wave's tokens
     const uint32_t of = wave * (64 / LPT) + at, n = lane_read(found, at * LPT);
     if (lane_read(whole, at * LPT) || n < r.k)
-      route_token<T>(r, first + of, keys64[wave]);
+      route_token<T>(r, first + of, keys64);
     else
-      order_candidates<T>(r, first + of, slot_id[of], n);
+      order_candidates<T>(r, first + of, slots + of * 2 * room, n);
     redo &= ~(kLanes << (at * LPT));
   }
 }
@@ -681,15 +682,20 @@ hipError_t launch_route(const void* logits, hc_dtype_t dtype, size_t ntokens, ui
   };
   auto run = [&](auto lpt, auto vals) {
     constexpr uint32_t LPT = decltype(lpt)::value, V = decltype(vals)::value;
+    // a wave's experts in 64 bits, and of each token candidates, keys and chosen logits
+    const uint32_t lds = 8 * kWaves * nexperts + 4 * (kThreads / LPT) * (2 * (r.k + kMore) + r.k);
     for (r.start = 0; r.start < ntokens; r.start += (size_t)kMaxBlocks * (kThreads / LPT)) {
       const uint32_t blocks = blocks_for(ntokens - r.start, kThreads / LPT);
-      if (dtype == HC_F32)
-        HC_ENQUEUE((route_kernel<F32, LPT, V>), blocks, kThreads, stream, r);
-      else
-        HC_ENQUEUE((route_kernel<BF16, LPT, V>), blocks, kThreads, stream, r);
+      const hipError_t e = dtype == HC_F32 ? enqueue_lds(lds, route_kernel<F32, LPT, V>, blocks, kThreads, stream, r)
+                                           : enqueue_lds(lds, route_kernel<BF16, LPT, V>, blocks, kThreads, stream, r);
+      if (e != hipSuccess) return e;
     }
     return hipSuccess;
   };
+  // 64 tokens of up to 16 experts, or 4 of HC_MAX_EXPERTS
+  static_assert(8 * kWaves * 16 + 4 * 64 * (3 * HC_MAX_TOPK + 2 * kMore) <= 64 << 10 &&
+                    8 * kWaves * HC_MAX_EXPERTS + 4 * 32 * (3 * HC_MAX_TOPK + 2 * kMore) <= 64 << 10,
+                "shared memory of a workgroup");
 #define HC_LANES(L, V) run(std::integral_constant<uint32_t, L>{}, std::integral_constant<uint32_t, V>{})
   uint32_t n = lanes(4);
   if (n <= 4) return HC_LANES(4, 4);
