@@ -172,6 +172,66 @@ def test_states_of_8_bits(types, seed, offset):
     case.check_guards()
 
 
+@pytest.mark.parametrize("seed", [0, 77])
+def test_states_by_single_operations(seed):
+    """m, v and the 8-bit codes are those of the operations as they are written,
+    each rounded once to fp32: numpy's, bit for bit."""
+    import numpy as np
+
+    f = np.float32
+    n = 200_000
+    for bits in (8, 32):
+        case = Case([n], (F,), (B,), bits, seed=12, offset=0)
+        g = case.grads[0].float().cpu().numpy() * f(0.25)
+        m, v = case.m[0].float().cpu().numpy(), case.v[0].float().cpu().numpy()
+        at = np.arange(n) // BLOCK
+        if bits == 8:
+            m = m * case.ms[0].cpu().numpy()[at]
+            v = v * case.vs[0].cpu().numpy()[at]
+            v = v * v
+        b1, a1, b2, a2 = f(0.9), f(1 - 0.9), f(0.99), f(1 - 0.99)
+        m = b1 * m + a1 * g
+        v = b2 * v + a2 * (g * g)
+        hc.hc_adamw(case.plan(), 4, lr=1e-3, betas=(0.9, 0.99), grad_scale=0.25, seed=seed)
+        if bits == 32:
+            assert np.array_equal(case.m[0].cpu().numpy(), m) and np.array_equal(case.v[0].cpu().numpy(), v)
+            continue
+        draw = random_bits(seed, 4, 0, n).numpy()
+        for x, codes, scales, cut in ((m, case.m[0], case.ms[0], 0), (np.sqrt(v), case.v[0], case.vs[0], 16)):
+            pad = np.zeros(-(-n // BLOCK) * BLOCK, f)
+            pad[:n] = x
+            unit = np.abs(pad).reshape(-1, BLOCK).max(1) * f(f(1) / f(448))
+            assert np.array_equal(scales.cpu().numpy(), unit)
+            y = np.clip(x / unit[at], f(-448), f(448))
+            if seed:
+                u = ((draw >> cut & 0xFFFF) + 0.5) / 65536
+                a = np.abs(y).astype(np.float64)
+                step = np.exp2(np.clip(np.frexp(a)[1] - 1, -6, None) - 3.0)
+                y = np.copysign(np.minimum(np.floor(a / step + u) * step, 448), y)
+            y = torch.from_numpy(np.asarray(y, f)).to(E4M3).float().numpy()
+            if cut:
+                y = np.where((x > 0) & (y == 0), f(2.0 ** -9), y)
+            assert np.array_equal(codes.cpu().float().numpy(), y), int((codes.cpu().float().numpy() != y).sum())
+
+
+def test_two_plans_of_the_same_tensors_and_two_streams():
+    """Plans of one set of tensors may be used in turn, and two of disjoint
+    tensors at once."""
+    a, b = (Case([70_000, 333], (F, B), (F,), 8, seed=s) for s in (1, 2))
+    c, d = (Case([70_000, 333], (F, B), (F,), 8, seed=s) for s in (1, 2))
+    pa, pa2, pb, pc, pd = a.plan(), a.plan(), b.plan(), c.plan(), d.plan()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for t in range(1, 6):
+        hc.hc_adamw(pa if t % 2 else pa2, t, seed=t, stream=one, **HYPER)
+        hc.hc_adamw(pb, t, seed=t, stream=two, **HYPER)
+    torch.cuda.synchronize()
+    for t in range(1, 6):
+        hc.hc_adamw(pc, t, seed=t, **HYPER)
+        hc.hc_adamw(pd, t, seed=t, **HYPER)
+    assert all(torch.equal(x[0], y[0]) for p, q in ((a, c), (b, d)) for x, y in zip(p.buffers, q.buffers))
+
+
 def test_bf16_parameters_by_random_bits():
     """Rounded up with the probability of what is cut off, by the bits that the
     definition names; the mean stays."""

@@ -259,6 +259,33 @@ def test_many_rows_and_the_same_bits_again():
     assert bool((dw == 0).all())
 
 
+@pytest.mark.parametrize("d", [1031, 2048, 5000])
+@pytest.mark.parametrize("dtype", [F, B])
+def test_large_batches_as_small_ones(d, dtype):
+    """Past 128 MiB rows are streamed: the same bits as of the rows in parts."""
+    g = gen(d)
+    t = (160 << 20) // (d * (4 if dtype == F else 2))
+    x, res = (torch.randn((t, d), generator=g, device="cuda").to(dtype) for _ in range(2))
+    w = torch.randn(d, generator=g, device="cuda")
+    out, s, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    q, scales = torch.empty((t, d), dtype=E4M3, device="cuda"), torch.empty((t, -(-d // 128)), device="cuda")
+    s8 = torch.empty_like(x)
+    hc.hc_rms_norm(x, w, out, residual=res, sum_out=s)
+    hc.hc_rms_norm_8bit(x, w, q, scales, group=128, residual=res, sum_out=s8)
+    hc.hc_rms_norm_grad(x, s, w, dx, dsum=res)
+    assert torch.equal(s, s8)
+    part = t // 7 + 1
+    for a in range(0, t, part):
+        b = slice(a, min(t, a + part))
+        o, h, o8, c = torch.empty_like(x[b]), torch.empty_like(x[b]), torch.empty_like(q[b]), torch.empty_like(scales[b])
+        hc.hc_rms_norm(x[b], w, o, residual=res[b], sum_out=h)
+        assert torch.equal(o, out[b]) and torch.equal(h, s[b])
+        hc.hc_rms_norm_8bit(x[b], w, o8, c, group=128, residual=res[b])
+        assert torch.equal(o8.view(torch.uint8), q[b].view(torch.uint8)) and torch.equal(c, scales[b])
+        hc.hc_rms_norm_grad(x[b], h, w, o, dsum=res[b])
+        assert torch.equal(o, dx[b])
+
+
 def test_offsets_past_32_bits():
     """Rows whose elements lie past 2^32 bytes and elements in."""
     t, d, stride = 3, 100, (1 << 31) + 11
