@@ -382,7 +382,15 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
           dw[u][i] = __builtin_fmaf(dy[i] * r, h[i], dw[u][i]);
           o[i] = __builtin_fmaf(r, __builtin_fmaf(-back, h[i], dy[i] * w[i]), o[i]);
         }
-        store_vec<T, NT>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(o));
+        // a vector moved back stores its own elements only: the others' dsum
+        // may be their dx already, another wave's
+        if (skip[u] == 0) {
+          store_vec<T, NT>(elem<T>(n.out, t * n.ostride + at[u]), T::pack(o));
+        } else {
+#pragma unroll
+          for (int i = 1; i < N; ++i)
+            if ((uint32_t)i >= skip[u]) *elem<T>(n.out, t * n.ostride + at[u] + i) = T::narrow(o[i]);
+        }
       }
     }
     if (!more) break;

@@ -167,6 +167,19 @@ def test_in_place(d, dtype):
         assert torch.equal(v[name], dx), name
 
 
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("d", [1, 3, 65, 129, 257, 511, 513, 1025, 2049, 4097, 4353, 8193, 8707, 16385, 16901])
+def test_gradient_onto_its_addend(d, dtype):
+    """dx is dsum where a row's last vector, moved back to its end, is another
+    wave's than the one before it, and where it is the same's."""
+    g = gen(d)
+    dy, h, ds = (rows(g, 19, d, dtype) for _ in range(3))
+    w, dx = torch.randn(d, generator=g, device="cuda"), torch.empty_like(dy)
+    hc.hc_rms_norm_grad(dy, h, w, dx, dsum=ds)
+    hc.hc_rms_norm_grad(dy, h, w, ds, dsum=ds)
+    assert torch.equal(ds, dx)
+
+
 def grads64(dy, h, w, eps, ds):
     """By torch's differentiation of the formula in 64 bits, and the sums of
     magnitudes that the roundings are relative to."""
