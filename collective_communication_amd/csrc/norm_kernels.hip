@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
         for (int i = 0; i < N; ++i) h[i] = prod[u][i] * lift * inv;
         store_codes<N, NT>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
         const uint32_t c = at[u] + skip[u];
-        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = peak[u] * (r * (1.0f / 448.0f));
+        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] =
+              peak[u] < __builtin_inff() ? peak[u] * (r * (1.0f / 448.0f)) : __builtin_nanf("");
       } else {
         T::unpack(v[u], h);
         load_weight<T>(n, at[u], w);

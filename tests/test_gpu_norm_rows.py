@@ -138,6 +138,12 @@ def test_tiny_and_odd_values(dtype):
     assert bool((out[1] == 0).all()) and bool((s[1] == 0).all()) and bool((q[1].float() == 0).all())
     assert bool(out[3].isnan().all()) and bool(s[3].isnan().all())
     assert bool((out[4, :299] == 0).all()) and bool(out[4, 299].isnan()) and bool(s[4, 2].isnan())
+    # a product that fp32 cannot hold, of finite values: its group is no number, the others are
+    x, big = torch.ones((1, 256), device="cuda"), torch.ones(256, device="cuda")
+    x[0, 7], big[7] = 2.0 ** 10, 2.0 ** 120
+    q, s = torch.empty((1, 256), dtype=E4M3, device="cuda"), torch.empty((1, 2), device="cuda")
+    hc.hc_rms_norm_8bit(x, big, q, s, group=128, eps=0.0)
+    assert bool(s[0, 0].isnan()) and bool(s[0, 1].isfinite()) and bool((q[0, 128:].float() == 448).all())
     # values whose t is far below what 448 / t can hold
     x = (torch.arange(1, 257, device="cuda", dtype=F) * 2.0 ** -126).view(1, 256)
     q, s = torch.empty((1, 256), dtype=E4M3, device="cuda"), torch.empty((1, 1), device="cuda")
@@ -170,14 +176,16 @@ def test_in_place(d, dtype):
 @pytest.mark.parametrize("dtype", [F, B])
 @pytest.mark.parametrize("d", [1, 3, 65, 129, 257, 511, 513, 1025, 2049, 4097, 4353, 8193, 8707, 16385, 16901])
 def test_gradient_onto_its_addend(d, dtype):
-    """dx is dsum where a row's last vector, moved back to its end, is another
-    wave's than the one before it, and where it is the same's."""
+    """dx is dsum, dout or h where a row's last vector, moved back to its end, is
+    another wave's than the one before it, and where it is the same's."""
     g = gen(d)
     dy, h, ds = (rows(g, 19, d, dtype) for _ in range(3))
     w, dx = torch.randn(d, generator=g, device="cuda"), torch.empty_like(dy)
     hc.hc_rms_norm_grad(dy, h, w, dx, dsum=ds)
-    hc.hc_rms_norm_grad(dy, h, w, ds, dsum=ds)
-    assert torch.equal(ds, dx)
+    for i in range(3):
+        v = [dy.clone(), h.clone(), ds.clone()]
+        hc.hc_rms_norm_grad(v[0], v[1], w, v[i], dsum=v[2])
+        assert torch.equal(v[i], dx), i
 
 
 def grads64(dy, h, w, eps, ds):
