@@ -30,6 +30,14 @@ hc_status_t check_norm_sizes(size_t ntokens, size_t dim, float eps) {
   return HC_SUCCESS;
 }
 
+// Rows that are written where others are read: the same rows, or apart.
+hc_status_t check_onto(const void* to, size_t tstride, const void* from, size_t fstride, size_t ntokens,
+                       const char* name) {
+  if (to == from && to && ntokens > 1 && tstride != fstride)
+    return fail(HC_ERR_INVALID_ARGUMENT, "%s: stride %zu on rows of stride %zu", name, tstride, fstride);
+  return HC_SUCCESS;
+}
+
 hc_status_t check_weight(const void* weight, hc_dtype_t type, const char* name) {
   HC_TRY(check_dtype(type, name));
   return check_ptr(weight, esize(type), name);
@@ -44,9 +52,17 @@ hc_status_t check_norm(const NormRows& a, bool out8) {
     if (!a.residual) return fail(HC_ERR_INVALID_ARGUMENT, "sum_out without a residual");
     HC_TRY(check_rows(a.sum, a.dtype, a.ntokens, a.dim, a.sstride, "sum_out"));
     if (a.ntokens && a.sum == a.out) return fail(HC_ERR_INVALID_ARGUMENT, "sum_out is out");
+    HC_TRY(check_onto(a.sum, a.sstride, a.x, a.xstride, a.ntokens, "sum_out"));
+    HC_TRY(check_onto(a.sum, a.sstride, a.residual, a.rstride, a.ntokens, "sum_out"));
   }
   HC_TRY(check_weight(a.weight, a.wtype, "weight"));
-  if (!out8) return check_rows(a.out, a.dtype, a.ntokens, a.dim, a.ostride, "out");
+  if (!out8) {
+    HC_TRY(check_rows(a.out, a.dtype, a.ntokens, a.dim, a.ostride, "out"));
+    HC_TRY(check_onto(a.out, a.ostride, a.x, a.xstride, a.ntokens, "out"));
+    return check_onto(a.out, a.ostride, a.residual, a.rstride, a.ntokens, "out");
+  }
+  if (a.ntokens && (a.out == a.x || a.out == a.residual || a.out == a.sum))
+    return fail(HC_ERR_INVALID_ARGUMENT, "out: rows of 8 bits where other rows are");
   if (a.ostride < a.dim || a.ostride > ((size_t)1 << 40))
     return fail(HC_ERR_INVALID_ARGUMENT, "out: stride %zu, width %zu", a.ostride, a.dim);
   return a.ntokens ? check_ptr(a.out, 1, "out") : HC_SUCCESS;
@@ -168,6 +184,9 @@ hc_status_t hc_rms_norm_grad(const void* dout, hc_dtype_t dtype, size_t ntokens,
   HC_TRY(check_weight(weight, weight_dtype, "weight"));
   if (dsum) HC_TRY(check_rows(dsum, dtype, ntokens, dim, dsum_stride, "dsum"));
   HC_TRY(check_rows(dx, dtype, ntokens, dim, dx_stride, "dx"));
+  HC_TRY(check_onto(dx, dx_stride, dout, dout_stride, ntokens, "dx"));
+  HC_TRY(check_onto(dx, dx_stride, h, h_stride, ntokens, "dx"));
+  HC_TRY(check_onto(dx, dx_stride, dsum, dsum_stride, ntokens, "dx"));
   if (dweight) {
     HC_TRY(check_weight(dweight, dweight_dtype, "dweight"));
     HC_TRY(check_ws(ws, ws_bytes, hc::rms_norm_grad_ws_bytes(ntokens, dim)));
@@ -204,6 +223,7 @@ hc_status_t hc_route_grad(const void* logits, hc_dtype_t dtype, size_t ntokens, 
   HC_TRY(check_route(ntokens, nexperts, opts));
   HC_TRY(check_rows(logits, dtype, ntokens, (size_t)nexperts, logits_stride, "logits"));
   HC_TRY(check_rows(dlogits, dtype, ntokens, (size_t)nexperts, dlogits_stride, "dlogits"));
+  HC_TRY(check_onto(dlogits, dlogits_stride, logits, logits_stride, ntokens, "dlogits"));
   if (ntokens) {
     HC_TRY(check_ptr(experts, 4, "experts"));
     HC_TRY(check_ptr(dweights, 4, "dweights"));

@@ -714,6 +714,8 @@ hc_status_t hc_expert_combine_grad(const void *dout, hc_dtype_t dtype, size_t di
  * an infinity has a scale that is NaN.  A row of 8 bits with its scales may go
  * through hc_expert_dispatch, two bytes as one bf16 element and a scale as fp32
  * (the rows are copied as they are).
+ *   out: apart from the other rows (HC_ERR_INVALID_ARGUMENT if it begins where
+ *     some of them do); sum_out may be x or residual.
  *   scales: ntokens rows of ceil(dim / group) (or 1) fp32, scales_stride apart.
  */
 #define HC_MAX_NORM_DIM 32768
@@ -733,7 +735,7 @@ hc_status_t hc_rms_norm_8bit(const void *x, hc_dtype_t dtype, size_t ntokens, si
  *     round(dweight + that sum)
  * in fp32; the order of the sums follows the sizes.
  *   dsum: the gradient that arrives at h beside the norm's, or NULL.  dx may
- *     be dout or dsum, with its stride.
+ *     be dout, h or dsum, with its stride.
  *   dweight: dim elements of dweight_dtype, or NULL (not computed).
  *   ws: hc_rms_norm_grad_workspace_bytes(ntokens, dim) bytes, which are enough
  *     for fewer tokens and columns as well (0 on invalid sizes); none is needed

@@ -25,7 +25,8 @@ def test_norm_refusals(hc):  # noqa: F811
     for bad in (dict(x=None), dict(x=P + 1), dict(dt=2), dict(dt=-1), dict(n=1 << 31), dict(d=0), dict(d=32769),
                 dict(xs=63), dict(xs=1 << 41), dict(r=Q + 1), dict(rs=63), dict(w=None), dict(w=W + 2), dict(wt=7),
                 dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(s=P + 4097), dict(ss=1), dict(o=None),
-                dict(o=P + 8193), dict(os=63), dict(r=None), dict(s=P + 8192)):
+                dict(o=P + 8193), dict(os=63), dict(r=None), dict(s=P + 8192),
+                dict(o=P, os=65), dict(o=Q, rs=65), dict(s=P, ss=72), dict(s=Q, ss=72)):
         assert call(**bad) == E, bad
     assert call(r=None) == E and b"residual" in L.hc_last_error()
     assert call(n=0, x=None, r=None, s=None, o=None) == 0
@@ -36,7 +37,7 @@ def test_norm_refusals(hc):  # noqa: F811
 
     for bad in (dict(x=None), dict(eps=NAN), dict(o=None), dict(os=63), dict(os=1 << 41), dict(group=1), dict(group=-1),
                 dict(group=96), dict(group=512), dict(scales=None), dict(scales=W + 2), dict(cs=0),
-                dict(group=32), dict(d=32769)):
+                dict(group=32), dict(d=32769), dict(o=P), dict(o=Q), dict(o=P + 4096)):
         assert call8(**bad) == E, bad
     assert call8(n=0, x=None, r=None, s=None, o=None, scales=None) == 0
 
@@ -61,6 +62,7 @@ def test_norm_gradient_refusals_and_workspace(hc):  # noqa: F811
 
     for bad in (dict(dy=None), dict(dy=P + 1), dict(dt=5), dict(ds=1), dict(h=None), dict(hs=63), dict(w=None),
                 dict(wt=9), dict(eps=-1.0), dict(add=Q + 1), dict(add=Q, adds=3), dict(dx=None), dict(dxs=2),
+                dict(dx=P, dxs=65), dict(dx=Q, hs=65), dict(add=P + 8192, adds=65),
                 dict(dw=W + 2), dict(dwt=4), dict(ws=None), dict(ws=W + 8), dict(d=0), dict(n=1 << 31)):
         assert call(**bad) == E, bad
     assert call(room=need - 1) == C
@@ -93,7 +95,7 @@ def test_route_refusals(hc):  # noqa: F811
     for bad in (dict(ngroups=0), dict(ngroups=3), dict(ngroups=65, e=65 * 4, s=65 * 4), dict(top_groups=0),
                 dict(top_groups=5), dict(group_best=0), dict(group_best=3), dict(k=9), dict(bias=W + 2)):
         assert call(**bad) == E, bad
-    assert grad(dx=None) == E and grad(dx=P + 1) == E and grad(ds=15) == E
+    assert grad(dx=None) == E and grad(dx=P + 1) == E and grad(ds=15) == E and grad(dx=P, ds=17) == E
     assert L.hc_route(P, 0, 4, 16, 16, None, Q, W, None) == E
     assert L.hc_route_grad(P, 0, 4, 16, 16, None, Q, W, P, 16, None) == E
     assert call(n=0, x=None, ids=None, w=None) == 0 and grad(n=0, x=None, ids=None, w=None, dx=None) == 0
