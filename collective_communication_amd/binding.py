@@ -793,17 +793,21 @@ class AdamWPlan:
 
     @classmethod
     def for_params(cls, params, grads, *, state_bits: int = 32, copies=None, decays=None, stream=None):
-        """A plan with states as they are before the first step."""
+        """A plan with states as they are before the first step, which `stream`
+        sees in order."""
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits {state_bits} is neither 8 nor 32")
         params = list(params)
         dtype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
         like = lambda p: torch.empty_like(p, dtype=dtype).zero_()  # noqa: E731
-        scales = lambda p: torch.zeros(-(-p.numel() // HC_STATE_BLOCK), device=p.device)  # noqa: E731
+        scales = lambda p: torch.zeros(-(-p.numel() // HC_STATE_BLOCK), dtype=torch.float32,  # noqa: E731
+                                       device=p.device)
         more = {} if state_bits == 32 else {"m_scales": [scales(p) for p in params],
                                             "v_scales": [scales(p) for p in params]}
-        return cls(params, grads, [like(p) for p in params], [like(p) for p in params], copies=copies, decays=decays,
-                   stream=stream, **more)
+        exp_avgs, exp_avg_sqs = [like(p) for p in params], [like(p) for p in params]
+        if stream is not None and params and params[0].is_cuda:
+            torch.cuda.ExternalStream(_raw_stream(stream)).wait_stream(torch.cuda.current_stream())
+        return cls(params, grads, exp_avgs, exp_avg_sqs, copies=copies, decays=decays, stream=stream, **more)
 
 
 def hc_adamw(plan: AdamWPlan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,

@@ -448,3 +448,27 @@ def test_large_tensor():
     assert bool(((got == want) | ((up - 1.0).abs() < 1e-3)).all())
     m = plan.exp_avgs[0][-5000:].float() * plan.m_scales[0][-40:].repeat_interleave(BLOCK)[-5000:]
     close(m, torch.full((5000,), 0.1), torch.full((5000,), 0.1 * 8 * U), "m")
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_plan_on_a_stream_of_its_own(bits):
+    """for_params and its first step on a stream that nothing else orders after
+    the states' zeroes, and under another default type."""
+    n = 1 << 24
+    p, g = torch.randn(n, device="cuda"), torch.randn(n, device="cuda")
+    want = p.clone()
+    hc.hc_adamw(hc.AdamWPlan.for_params([want], [g], state_bits=bits), 1)
+    got = p.clone()
+    junk = [torch.full((n,), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    del junk                                             # memory that the states may get
+    side = torch.cuda.Stream()
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        plan = hc.AdamWPlan.for_params([got], [g], state_bits=bits, stream=side)
+    finally:
+        torch.set_default_dtype(before)
+    hc.hc_adamw(plan, 1, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
