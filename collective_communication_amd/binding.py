@@ -818,8 +818,8 @@ def hc_adamw(plan: AdamWPlan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float =
     The gradients are scaled by grad_scale and, with d_norm (their norm before
     that), clipped to max_norm.  seed: 0 rounds to nearest, else 8-bit states
     and bf16 parameters are rounded by random bits."""
-    st = (_native or _load_native()).adamw(plan._at, step, lr, betas[0], betas[1], eps, weight_decay, grad_scale,
-                                           d_norm, max_norm, seed, skip_nonfinite, _raw_stream(stream))
+    st = (_native or _load_native()).adamw(plan._at, plan.table, step, lr, betas[0], betas[1], eps, weight_decay,
+                                           grad_scale, d_norm, max_norm, seed, skip_nonfinite, _raw_stream(stream))
     if st:
         _check(st)
 

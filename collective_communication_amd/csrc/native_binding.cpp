@@ -518,31 +518,32 @@ const void* scalar(PyObject* o, at::ScalarType type, const char* name) {
   return flat(o, 1, name);
 }
 
-// plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, d_norm, max_norm, seed, skip_nonfinite, stream
+// plan, table, step, lr, beta1, beta2, eps, weight_decay, grad_scale, d_norm, max_norm, seed, skip_nonfinite, stream
 // (step and lr: numbers or device scalars)
 hc_status_t adamw(Args a) {
   const hc_adamw_plan_t* plan = static_cast<const hc_adamw_plan_t*>(PyLong_AsVoidPtr(a[0]));
   if (!plan && PyErr_Occurred()) throw PyError{};
+  here(tensor(a[1], "table"), "the plan");
   hc_adamw_opts_t o = {};
-  if (THPVariable_Check(a[1]))
-    o.d_step = static_cast<const int64_t*>(scalar(a[1], at::kLong, "step"));
-  else
-    o.step = integer(a[1]);
   if (THPVariable_Check(a[2]))
-    o.d_lr = static_cast<const float*>(scalar(a[2], at::kFloat, "lr"));
+    o.d_step = static_cast<const int64_t*>(scalar(a[2], at::kLong, "step"));
   else
-    o.lr = number(a[2]);
-  o.beta1 = number(a[3]);
-  o.beta2 = number(a[4]);
-  o.eps = number(a[5]);
-  o.weight_decay = number(a[6]);
-  o.grad_scale = (float)number(a[7]);
-  o.d_norm = static_cast<const float*>(scalar(a[8], at::kFloat, "d_norm"));
-  o.max_norm = (float)number(a[9]);
-  o.seed = PyLong_AsUnsignedLongLong(a[10]);
+    o.step = integer(a[2]);
+  if (THPVariable_Check(a[3]))
+    o.d_lr = static_cast<const float*>(scalar(a[3], at::kFloat, "lr"));
+  else
+    o.lr = number(a[3]);
+  o.beta1 = number(a[4]);
+  o.beta2 = number(a[5]);
+  o.eps = number(a[6]);
+  o.weight_decay = number(a[7]);
+  o.grad_scale = (float)number(a[8]);
+  o.d_norm = static_cast<const float*>(scalar(a[9], at::kFloat, "d_norm"));
+  o.max_norm = (float)number(a[10]);
+  o.seed = PyLong_AsUnsignedLongLong(a[11]);
   if (o.seed == ~0ull && PyErr_Occurred()) throw PyError{};
-  o.skip_nonfinite = integer(a[11]) != 0;
-  return hc_adamw(plan, &o, stream_of(a[12]));
+  o.skip_nonfinite = integer(a[12]) != 0;
+  return hc_adamw(plan, &o, stream_of(a[13]));
 }
 
 // Runs one of the functions above: its status as an int, or a Python error.
@@ -579,7 +580,7 @@ PyMethodDef methods[] = {
     HC_METHOD(expert_dispatch, 4), HC_METHOD(expert_combine, 5), HC_METHOD(expert_combine_grad, 7),
     HC_METHOD(rms_norm, 7),        HC_METHOD(rms_norm_8bit, 9),  HC_METHOD(rms_norm_grad, 10),
     HC_METHOD(route, 11),          HC_METHOD(route_grad, 8),     HC_METHOD(adamw_plan, 11),
-    HC_METHOD(adamw, 13),
+    HC_METHOD(adamw, 14),
     {"is_dense", is_dense, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
