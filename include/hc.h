@@ -827,7 +827,7 @@ hc_status_t hc_route_grad(const void *logits, hc_dtype_t dtype, size_t ntokens, 
  *     value = code * scale, scale = largest magnitude of the block * (1 / 448) (0
  *     for a block of zeroes, or of magnitudes below 2^-100).  The step's own p is computed
  *     from m and v before they are rounded; a root that is not 0 is never
- *     stored as 0.  Codes and scales of zero are the state before step 1.
+ *     stored as 0.  A v past fp32 is NaN, in its p too (in 32 bits it is infinite).  Codes and scales of zero are the state before step 1.
  *   copies: NULL, or an entry per tensor: NULL, or count bf16 values that
  *     receive the updated fp32 parameter, rounded to nearest.
  *   decays: NULL (all 1), or the factor of weight_decay per tensor.
@@ -836,7 +836,8 @@ hc_status_t hc_route_grad(const void *logits, hc_dtype_t dtype, size_t ntokens, 
  *
  * hc_adamw_opts_t:
  *   step >= 1, or d_step, a device int64 that is read instead (a captured
- *     launch then follows it); lr, or d_lr, a device fp32.
+ *     launch then follows it; one below 1 makes the parameters NaN); lr, or
+ *     d_lr, a device fp32.
  *   d_norm: device fp32, the norm of the gradients before grad_scale, to clip
  *     by; NULL: no clipping, c = grad_scale.  max_norm >= 0.
  *   skip_nonfinite: with d_norm, a norm that is infinite or NaN leaves
