@@ -240,10 +240,37 @@ __device__ __forceinline__ float value32(uint32_t o) {
 
 constexpr uint32_t kMore = 8;             // candidates past the k-th
 
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+  const uint32_t low = min(a, b);
+  a = max(a, b);
+  b = low;
+}
+// The four largest of V (a multiple of 4) keys, the largest first: by fours, each joined
+// to those before by the larger of opposite places.
+template <uint32_t V>
+__device__ __forceinline__ void largest4(const uint32_t (&key)[V], uint32_t (&best)[4]) {
+#pragma unroll
+  for (uint32_t v = 0; v < V; v += 4) {
+    uint32_t k[4] = {key[v], key[v + 1], key[v + 2], key[v + 3]};
+    order(k[0], k[1]);
+    order(k[2], k[3]);
+    order(k[0], k[2]);
+    order(k[1], k[3]);
+    order(k[1], k[2]);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) best[i] = v ? max(best[i], k[3 - i]) : k[i];
+    if (v == 0) continue;
+    order(best[0], best[2]);
+    order(best[1], best[3]);
+    order(best[0], best[1]);
+    order(best[2], best[3]);
+  }
+}
+
 // A token by LPT neighbouring lanes, V experts in a row each (a group by
 // group_lanes of them), as 32-bit keys: the choice value's upper bits and, in
-// the lowest, which of the lane's it is, so that a lane's largest is found by
-// one maximum per value, and its next by the largest below it.  Where values
+// the lowest, which of the lane's it is: a lane orders its four largest, and
+// few tokens want a fifth of one lane.  Where values
 // that decide are nearer than these keys and fp32's exponentials tell apart, the
 // wave orders the token's candidates in 64 bits, and where these are not
 // certain (groups, a NaN, many values nearly alike) takes the whole token so.
@@ -354,23 +381,18 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
   constexpr float kCut = V * 0x1p-23f;
   const float unit = 0x1p-20f * (softmax ? 1.0f / z : 1.0f);
   auto off = [=](float c) { return fabsf(c) * (kCut + 0x1p-23f) + unit; };
-  // a lane's largest key below `limit` + 1
-  uint32_t limit = ~0u;
-  auto largest = [&] {
+  uint32_t top4[4];
+  largest4<V>(key, top4);
+  // a lane's largest key up to `limit`, for the few that four are not enough for
+  auto largest = [&](uint32_t limit) {
     uint32_t d = limit;
 #pragma unroll
     for (uint32_t v = 0; v < V; ++v) d = min(d, limit - key[v]);     // wraps far up for those above
     return limit - d;
   };
-  uint32_t best = largest();
   if (r.groups > 1) {
     // the two largest keys of the lane's group
-    uint32_t a = best, b = 0;
-    if (r.group_best == 2) {
-      limit = best - 1;
-      b = largest();
-      limit = ~0u;
-    }
+    uint32_t a = top4[0], b = top4[1];
     for (uint32_t m = 1; m < r.group_lanes; m <<= 1) {
       const uint32_t a2 = (uint32_t)__shfl_xor((int)a, (int)m), b2 = (uint32_t)__shfl_xor((int)b, (int)m);
       b = max(max(b, b2), min(a, a2));
@@ -411,20 +433,15 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
     if (__any(close && live)) {
       // the groups' values in 64 bits, of each lane's two largest; where its third
       // may be among them, or with a row's sum to take, the whole token
-      limit = best - 1;
-      const uint32_t next = largest();
-      limit = next - 1;
-      const uint32_t third = next ? largest() : 0;
-      limit = ~0u;
-      const float c2 = value32(next & ~(V - 1)), c3 = value32(third & ~(V - 1));
-      const bool sure = third < kChoosable || c2 - c3 > 2.0f * (near + off(c2));
+      const float c2 = value32(top4[1] & ~(V - 1)), c3 = value32(top4[2] & ~(V - 1));
+      const bool sure = top4[2] < kChoosable || c2 - c3 > 2.0f * (near + off(c2));
       auto exactly = [&](uint32_t k) {
         const uint32_t e = e0 + (k >= kChoosable ? (V - 1) - (k & (V - 1)) : 0);
         const double v = T::widen(row[e]);
         const double s = by_score || r.group_best == 2 ? 1.0 / (1.0 + exp(-v)) + (by_score ? (double)r.bias[e] : 0.0) : v;
         return k >= kChoosable ? s : -__builtin_inf();
       };
-      double d = exactly(best), d2 = exactly(next);
+      double d = exactly(top4[0]), d2 = exactly(top4[1]);
       if (d2 > d) {
         const double swap = d;
         d = d2;
@@ -442,15 +459,14 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
         if (softmax || !sure) odd = true;
       }
     }
-    if (!kept) limit = 0;                   // no key of the lane's is below it
-    best = largest();
+    if (!kept) top4[0] = 0;                 // never taken, and so none after it
   }
   // the k largest, and those after that may belong to them
   const uint32_t picks = exact ? r.k : r.k + kMore;
   uint32_t found = 0, before = 0;
   bool open = !exact;        // whether the next may still belong to them
   for (uint32_t j = 0; j < picks; ++j) {
-    const uint32_t m = max_token<LPT>(best);
+    const uint32_t best = top4[0], m = max_token<LPT>(best);
     const bool there = m >= kChoosable;
     if (j >= r.k) {
       const float c = value32(before & ~(V - 1)), c2 = value32(m & ~(V - 1));
@@ -472,8 +488,11 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
     if (take && winner == lane) {
       ids[j] = e0 + (V - 1) - (best & (V - 1));
       keep[j] = best;
-      limit = best - 1;
-      best = largest();
+      top4[0] = top4[1];
+      top4[1] = top4[2];
+      top4[2] = top4[3];
+      top4[3] = 0;
+      if (V > 4 && top4[0] == 0) top4[0] = largest(best - 1);
     }
   }
   // more candidates than there was room for, or than a wave has lanes
