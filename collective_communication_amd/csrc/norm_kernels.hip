@@ -405,9 +405,14 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
   if constexpr (RPW == 1) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (N > 1 && skip[u] == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if ((uint32_t)i >= skip[u]) to[at[u] + i] = dw[u][i];
+        for (int i = 0; i + 4 <= N; i += 4) store_vec<F32>(elem<F32>(to, at[u] + i), F32::pack(dw[u] + i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if ((uint32_t)i >= skip[u]) to[at[u] + i] = dw[u][i];
+      }
     }
   } else {
     constexpr uint32_t wide = LPR * U * N;
