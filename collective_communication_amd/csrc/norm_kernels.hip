@@ -565,8 +565,12 @@ hipError_t launch_rms_norm_grad(const NormRows& a, const void* dout, size_t dstr
       constexpr uint32_t LPR = decltype(lanes)::value, TH = threads_of<LPR>();
       constexpr int U = decltype(vecs)::value;
       const uint64_t groups = (n.ntokens + TH / LPR - 1) / (TH / LPR);
-      constexpr uint32_t most = kPartials * kThreads / TH;     // as many waves, and fewer partials of wider rows
-      rows = (uint32_t)(groups < most ? groups : most);
+      // As many waves, and fewer partials of wider rows.  Two rows a workgroup before
+      // there are 8 waves a CU more: 500 x 2560 fp32 10.5 us by 256 workgroups, 11.8 by
+      // 500; 1000 x 2048 bf16 9.8 and 12.4.  Not where a row waits for the one before
+      // it: 200 x 12,000 bf16 14.2 by 128, 13.9 by 200.
+      constexpr uint32_t most = kPartials * kThreads / TH, few = LPR < 1024 ? most / 2 : most;
+      rows = (uint32_t)(groups <= few ? groups : groups >= 2 * most ? most : groups <= 2 * few ? few : (groups + 1) / 2);
       // rows read once, which the step before has mostly left in memory from here on
       if (n.ntokens * n.dim * sizeof(typename T::raw) >= kStreamStoreBytes)
         HC_ENQUEUE((norm_grad_kernel<T, LPR, U, true>), rows, TH, stream, n);
