@@ -88,9 +88,14 @@ __device__ __forceinline__ void load_weight(const Norm& n, uint32_t c, float* w)
   }
 }
 
-// The largest of `lanes` (4 to 64) neighbouring lanes' values.
+// The larger of two values that are not negative; a NaN is above all.
+struct MaxBits {
+  __device__ __forceinline__ float operator()(float a, float b) const { return bits_f32(max(f32_bits(a), f32_bits(b))); }
+};
+
+// The largest of `lanes` (4 to 64) neighbouring lanes' values, none negative.
 __device__ __forceinline__ float max_lanes(float v, uint32_t lanes) {
-  auto op = [](uint32_t a, uint32_t b) { return f32_bits(MaxOp{}(bits_f32(a), bits_f32(b))); };
+  auto op = [](uint32_t a, uint32_t b) { return max(a, b); };
   uint32_t x = join_lanes<4>(f32_bits(v), op);
   if (lanes > 4) x = join_step<4>(x, op);
   if (lanes > 8) x = join_step<8>(x, op);
@@ -246,13 +251,13 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             prod[u][i] = h[i] * w[i];
-            if ((uint32_t)i >= skip[u]) peak[u] = MaxOp{}(fabsf(prod[u][i]), peak[u]);
+            if ((uint32_t)i >= skip[u]) peak[u] = MaxBits{}(fabsf(prod[u][i]), peak[u]);
           }
         }
-        top = MaxOp{}(peak[u], top);
+        top = MaxBits{}(peak[u], top);
       }
     }
-    join_row<LPR, SumOp, MaxOp>(squares, top, lds[turn]);
+    join_row<LPR, SumOp, MaxBits>(squares, top, lds[turn]);
     turn ^= 1;
     const float r = inverse<LPR>(n, squares, [&] {
       float sum = small_squares<T, U>(v, skip), none = 0.0f;

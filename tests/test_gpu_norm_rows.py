@@ -144,6 +144,17 @@ def test_tiny_and_odd_values(dtype):
     q, s = torch.empty((1, 256), dtype=E4M3, device="cuda"), torch.empty((1, 2), device="cuda")
     hc.hc_rms_norm_8bit(x, big, q, s, group=128, eps=0.0)
     assert bool(s[0, 0].isnan()) and bool(s[0, 1].isfinite()) and bool((q[0, 128:].float() == 448).all())
+    # a weight that is no number, or infinite: its group is none, the others and a moved-back vector's are
+    for d, at in ((261, 7), (261, 254), (300, 255), (131, 127)):
+        for bad in (math.nan, math.inf):
+            x, big = torch.ones((1, d), device="cuda"), torch.ones(d, device="cuda")
+            big[at] = bad
+            for dtype in (F, B):
+                q, s = torch.empty((1, d), dtype=E4M3, device="cuda"), torch.empty((1, -(-d // 128)), device="cuda")
+                hc.hc_rms_norm_8bit(x.to(dtype), big, q, s, group=128, eps=0.0)
+                assert s[0].isnan().nonzero().view(-1).tolist() == [at // 128], (d, at, bad, dtype)
+                other = torch.arange(d, device="cuda") // 128 != at // 128
+                assert bool((q[0].float()[other] == 448).all()), (d, at, bad, dtype)
     # values whose t is far below what 448 / t can hold
     x = (torch.arange(1, 257, device="cuda", dtype=F) * 2.0 ** -126).view(1, 256)
     q, s = torch.empty((1, 256), dtype=E4M3, device="cuda"), torch.empty((1, 1), device="cuda")
