@@ -13,13 +13,14 @@
 // partials per workgroup, which a second launch adds in a fixed order.
 //
 // Measured (a large copy reaches 4.8-5.2 TB/s here): 16,384 x 4096 bf16 with a residual
-// to 8 bits, a scale for 128 columns (472 MB) 91 us, 5.2 TB/s (105 with plain
+// to 8 bits, a scale for 128 columns (472 MB) 92 us, 5.1 TB/s (105 with plain
 // stores and joins through shared memory, 111 by 8 waves a row, 126 by 2); 60,000 x
-// 2048 without a residual, which is bound by the lanes' work, 110 us (131 with full
+// 2048 without a residual, which is bound by the lanes' work, 106 us (131 with full
 // divisions and each product made twice).  Its gradient with dsum, 16,384 x
-// 4096 (537 MB) 97 us, 5.5 TB/s, and 7 for the weight's partials: 118 without the
-// next row's loads ahead, or with them and 130 registers instead of 128.
-// 64 x 4096 to 8 bits 4.5 us, 500 x 2560 fp32 gradient 6.8 + 6.1.
+// 4096 (537 MB) 92 us, 5.8 TB/s, and 7 for the weight's partials: 97 with these
+// stored by single values, 118 without the next row's loads ahead, or with them and
+// 130 registers instead of 128.  64 x 4096 to 8 bits 4.3 us, 500 x 2560 fp32
+// gradient 6.5 + 4.2.
 #include <type_traits>
 
 #include "arith.hpp"

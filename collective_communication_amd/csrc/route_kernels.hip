@@ -11,9 +11,10 @@
 // bits (about one token in 300 with 256 sigmoid scores, by its few candidates).
 //
 // Measured: 32,768 tokens, 256 experts, fp32 logits, a bias, 8 of 4 of 8 groups
-// (35 MB) 22 us, of which some 8 are the picks and the groups, 5 the 64 bits
-// and their registers; each token in 64 bits by a wave 152 us.  64 tokens, 8 of
-// 128: 4.4 us.
+// (35 MB) 21 us, 230 instructions a token, of which some 6 are the picks and the
+// groups, 4 the 64 bits and their registers (22.5 with each pick's next largest
+// searched among the lane's 16; 7 or 8 waves a SIMD instead of 6: 22.2, 21.4, with
+// registers spilled); each token in 64 bits by a wave 152 us.  64 tokens, 8 of 128: 4.4 us.
 #include <type_traits>
 
 #include "lanes.hpp"
