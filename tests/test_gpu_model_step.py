@@ -4,12 +4,13 @@ ranks alike to the bit whatever the optimizer, and rows of 8 bits sent to their
 experts."""
 import os
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
 
 from collective_communication_amd import binding as hc
-from test_gpu_step_ops import U, close, gen, space
+from test_gpu_step_ops import B, U, close, gen, space
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
@@ -165,3 +166,37 @@ def test_a_captured_step():
         torch.cuda.synchronize()
         b.step()
         assert all(torch.equal(p, q) for p, q in zip(a.all(), b.all())), i
+
+
+def test_two_threads_at_once():
+    """Two host threads, a stream, tensors and a plan each, in calls of all the
+    operators at once: what each computes alone."""
+    t, d, n, k = 300, 512, 48, 4
+
+    def work(seed, stream):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x, res = (torch.randn((t, d), generator=g, device="cuda").to(B) for _ in range(2))
+        w, logits = torch.randn(d, generator=g, device="cuda"), torch.randn((t, n), generator=g, device="cuda")
+        p = torch.randn(5000, generator=g, device="cuda").to(B)
+        out, s, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+        ws = torch.empty(hc.hc_rms_norm_grad_workspace_bytes(t, d), dtype=torch.uint8, device="cuda")
+        e = torch.empty((t, k), dtype=torch.int32, device="cuda")
+        c, dl = torch.empty((t, k), device="cuda"), torch.empty_like(logits)
+        plan = hc.AdamWPlan.for_params([p], [torch.randn(5000, generator=g, device="cuda")], state_bits=8)
+        torch.cuda.synchronize()
+        for i in range(30):
+            hc.hc_rms_norm(x, w, out, residual=res, sum_out=s, stream=stream)
+            hc.hc_rms_norm_grad(out, s, w, dx, dw, ws, dsum=res, stream=stream)
+            hc.hc_route(logits, e, c, scores="sigmoid", bias=w[:n], groups=4, top_groups=2, group_best=2, stream=stream)
+            hc.hc_route_grad(logits, e, c, dl, scores="sigmoid", stream=stream)
+            hc.hc_adamw(plan, i + 1, seed=seed, stream=stream)
+            with pytest.raises(hc.HcError, match="step 0" if seed == 1 else "eps"):
+                hc.hc_adamw(plan, 0) if seed == 1 else hc.hc_adamw(plan, 1, eps=-1.0)
+        stream.synchronize()
+        return [out, s, dx, dw, e, c, dl, p]
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want = [work(i + 1, streams[i]) for i in range(2)]
+    with ThreadPoolExecutor(2) as pool:
+        got = list(pool.map(work, (1, 2), streams))
+    assert all(torch.equal(a, b) for i in range(2) for a, b in zip(got[i], want[i]))
