@@ -9,6 +9,7 @@ is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Sequence
@@ -761,6 +762,13 @@ def hc_adamw_table_bytes(ntensors: int) -> int:
     return int(load().hc_adamw_table_bytes(ntensors))
 
 
+def _allocating_on(stream, device):
+    """Memory of `stream` (an object, a raw handle, or None for the current one) within."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
 class AdamWPlan:
     """The tensors of an AdamW step (hc_adamw_plan_t) and their table on the
     device, for as long as the tensors stay where they are.  Gradients, states
@@ -770,7 +778,14 @@ class AdamWPlan:
     States of 32 bits are float32; with m_scales and v_scales they are 8 bits
     (float8_e4m3fn or uint8 codes), a float32 scale for every HC_STATE_BLOCK
     values.  copies: bfloat16 copies of float32 parameters, or None each.
-    decays: factors of the weight decay.  ``for_params`` makes zero states."""
+    decays: factors of the weight decay.  ``for_params`` makes zero states.
+
+    What the plan allocates itself (the table unless one is given, and the
+    states of ``for_params``) is memory of `stream`, or of the current stream,
+    and is known to every stream of torch's that a step runs on: a plan may be
+    dropped while its steps are pending.  Where a step ran on another stream
+    that is not torch's (a raw handle, an ExternalStream), which may be gone
+    before the plan is, the plan is kept until that step is done."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_scales=None, copies=None, decays=None,
                  table: torch.Tensor | None = None, stream=None):
@@ -780,9 +795,13 @@ class AdamWPlan:
         self.m_scales = None if m_scales is None else list(m_scales)
         self.v_scales = None if v_scales is None else list(v_scales)
         self.copies = None if copies is None else list(copies)
+        self._own, self._known = [], set()      # memory of its own, and the handles of torch's streams that know it
         if table is None:
-            device = self.params[0].device if self.params else "cuda"
-            table = torch.empty(hc_adamw_table_bytes(len(self.params)), dtype=torch.uint8, device=device)
+            device = self.params[0].device if self.params else torch.device("cuda")
+            # of the pool of the stream that it is written on: nothing pending elsewhere may still use it
+            with _allocating_on(stream, device):
+                table = torch.empty(hc_adamw_table_bytes(len(self.params)), dtype=torch.uint8, device=device)
+            self._own.append(table)
         self.table = table
         self._c = hc_adamw_plan_t()
         self._at = ctypes.addressof(self._c)
@@ -793,8 +812,8 @@ class AdamWPlan:
 
     @classmethod
     def for_params(cls, params, grads, *, state_bits: int = 32, copies=None, decays=None, stream=None):
-        """A plan with states as they are before the first step, which `stream`
-        sees in order."""
+        """A plan with states as they are before the first step; `stream` and
+        the current stream wait for one another, so that both see them."""
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits {state_bits} is neither 8 nor 32")
         params = list(params)
@@ -802,12 +821,34 @@ class AdamWPlan:
         like = lambda p: torch.empty_like(p, dtype=dtype).zero_()  # noqa: E731
         scales = lambda p: torch.zeros(-(-p.numel() // HC_STATE_BLOCK), dtype=torch.float32,  # noqa: E731
                                        device=p.device)
-        more = {} if state_bits == 32 else {"m_scales": [scales(p) for p in params],
-                                            "v_scales": [scales(p) for p in params]}
-        exp_avgs, exp_avg_sqs = [like(p) for p in params], [like(p) for p in params]
-        if stream is not None and params and params[0].is_cuda:
-            torch.cuda.ExternalStream(_raw_stream(stream)).wait_stream(torch.cuda.current_stream())
-        return cls(params, grads, exp_avgs, exp_avg_sqs, copies=copies, decays=decays, stream=stream, **more)
+        device = params[0].device if params else torch.device("cpu")
+        here = torch.cuda.current_stream() if stream is not None and device.type == "cuda" else None
+        with _allocating_on(stream, device):
+            if here is not None:
+                torch.cuda.current_stream().wait_stream(here)
+            more = {} if state_bits == 32 else {"m_scales": [scales(p) for p in params],
+                                                "v_scales": [scales(p) for p in params]}
+            exp_avgs, exp_avg_sqs = [like(p) for p in params], [like(p) for p in params]
+            if here is not None:
+                here.wait_stream(torch.cuda.current_stream())
+        plan = cls(params, grads, exp_avgs, exp_avg_sqs, copies=copies, decays=decays, stream=stream, **more)
+        plan._own += exp_avgs + exp_avg_sqs + [s for one in more.values() for s in one]
+        return plan
+
+    def _ran_on(self, stream):
+        """After a step on `stream`: the plan's own memory is not given to
+        another use before that step is done."""
+        if isinstance(stream, int) or not self._own:
+            return
+        raw = _stream_handle(stream)
+        if raw in self._known:
+            return
+        s = torch.cuda.current_stream() if stream is None else stream
+        if raw and s.stream_id == raw:          # not one of torch's own, which last as long as the process
+            return
+        for t in self._own:
+            t.record_stream(s)
+        self._known.add(raw)
 
 
 def hc_adamw(plan: AdamWPlan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
@@ -822,6 +863,7 @@ def hc_adamw(plan: AdamWPlan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float =
                                            grad_scale, d_norm, max_norm, seed, skip_nonfinite, _raw_stream(stream))
     if st:
         _check(st)
+    plan._ran_on(stream)
 
 
 # ----------------------------------------------------------------------------- streams

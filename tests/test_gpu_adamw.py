@@ -472,3 +472,56 @@ def test_plan_on_a_stream_of_its_own(bits):
     hc.hc_adamw(plan, 1, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_plans_made_and_dropped_while_streams_are_busy():
+    """A plan made on a stream while kernels of the current one still write to
+    memory that was freed there, stepped and dropped at once, and another use of
+    what it had."""
+    sizes = [5000, 130, 40_000]
+    n = hc.hc_adamw_table_bytes(len(sizes))
+    side = torch.cuda.Stream()
+    assert side.stream_id != side.cuda_stream
+    outside = torch.cuda.ExternalStream(side.cuda_stream)
+    assert outside.stream_id == outside.cuda_stream       # how the binding tells torch's streams from others
+    for bits in (8, 32):
+        want = Case(sizes, (F, B), (F,), bits, seed=21)
+        hc.hc_adamw(want.plan(), 1, **HYPER)
+        for made, run in ((side, side), (side.cuda_stream, side.cuda_stream), (None, side), (side, None), (None, None)):
+            case = Case(sizes, (F, B), (F,), bits, seed=21)
+            torch.cuda.synchronize()
+            junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            torch.cuda._sleep(2_000_000)
+            for j in junk:
+                j.fill_(0)
+            del junk, j
+            plan = case.plan(stream=made)
+            if made is not run:                           # the step after the table's writing
+                torch.cuda.synchronize()
+            with torch.cuda.stream(side if run is not None else torch.cuda.current_stream()):
+                torch.cuda._sleep(2_000_000)
+            hc.hc_adamw(plan, 1, stream=run, **HYPER)
+            del plan
+            junk = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            with torch.cuda.stream(side):
+                more = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            torch.cuda.synchronize()
+            del junk, more
+            assert all(torch.equal(x[0], y[0]) for x, y in zip(case.buffers, want.buffers)), (bits, made, run)
+    # states of for_params, dropped with a step pending
+    g = gen(22)
+    p, grad = torch.randn(100_000, generator=g, device="cuda"), torch.randn(100_000, generator=g, device="cuda")
+    want = p.clone()
+    hc.hc_adamw(hc.AdamWPlan.for_params([want], [grad]), 1)
+    for made, run in ((side, side), (None, side)):
+        got = p.clone()
+        plan = hc.AdamWPlan.for_params([got], [grad], stream=made)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        hc.hc_adamw(plan, 1, stream=run)
+        del plan
+        junk = [torch.full((100_000,), math.nan, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        assert torch.equal(got, want), (made, run)

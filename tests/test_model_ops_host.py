@@ -188,3 +188,97 @@ def test_binding_refuses_host_tensors_and_wrong_types(hc):  # noqa: F811
         hc.AdamWPlan.for_params([x], [x], state_bits=16)
     with pytest.raises(ValueError, match="gaps"):
         hc.AdamWPlan([x[:, ::2]], [x], [x], [x])
+
+
+def test_plan_memory_and_streams(hc, monkeypatch):  # noqa: F811
+    """What a plan allocates is memory of the stream that it is made on, and is
+    recorded on torch's other streams that run it: the calls that torch gets."""
+    import contextlib
+
+    class Stream:
+        def __init__(self, handle, own=True):
+            self.cuda_stream, self.stream_id = handle, 3 if own else handle
+            self.waits = []
+
+        def wait_stream(self, other):
+            self.waits.append(other)
+
+    class Native:
+        def __init__(self):
+            self.streams = []
+
+        def adamw_plan(self, *a):
+            self.streams.append(a[-1])
+            return 0
+
+        def adamw(self, *a):
+            self.streams.append(a[-1])
+            return 0
+
+    class Fake:
+        def __init__(self, n):
+            self.n, self.is_cuda, self.device = n, True, torch.device("cuda", 0)
+
+        def numel(self):
+            return self.n
+
+    now, made, recorded = [Stream(0)], [], []
+
+    class Memory:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, *a, **k):
+            made.append((self, now[-1]))
+
+        def zero_(self):
+            return self
+
+        def record_stream(self, s):
+            recorded.append((self, s))
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    native = Native()
+    monkeypatch.setattr(hc, "_native", native)
+    for name in ("empty", "empty_like", "zeros"):
+        monkeypatch.setattr(torch, name, Memory)
+    external = {}
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: external.setdefault(h, Stream(h, False)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(hc, "_current_stream_handle", lambda: now[-1].cuda_stream)
+    side, other = Stream(0x100), Stream(0x200)
+    x = [Fake(5)]
+    # a table by itself, by an object and by a handle
+    plan = hc.AdamWPlan(x, x, x, x, stream=side)
+    assert [s for _, s in made] == [side] and native.streams == [0x100]
+    hc.AdamWPlan(x, x, x, x, stream=0x300)
+    assert made[-1][1] is external[0x300] and native.streams[-1] == 0x300
+    hc.AdamWPlan(x, x, x, x)
+    assert made[-1][1] is now[0]
+    mine = Memory()
+    given = hc.AdamWPlan(x, x, x, x, table=mine, stream=side)
+    assert given.table is mine and made[-1][0] is mine
+    # steps: each of torch's streams once, no other's, and not what the caller owns
+    for _ in range(2):
+        hc.hc_adamw(plan, 1, stream=side)
+        hc.hc_adamw(plan, 1, stream=other)
+        hc.hc_adamw(plan, 1)
+        hc.hc_adamw(plan, 1, stream=0x300)
+        hc.hc_adamw(plan, 1, stream=external[0x300])
+        hc.hc_adamw(given, 1, stream=other)
+    assert recorded == [(plan.table, side), (plan.table, other), (plan.table, now[0])]
+    # for_params: its states, which both streams see
+    for bits, n in ((32, 3), (8, 5)):
+        made.clear(), recorded.clear(), now[0].waits.clear()
+        plan = hc.AdamWPlan.for_params(x, x, state_bits=bits, stream=side)
+        assert len(made) == n and all(s is side for _, s in made) and now[0].waits == [side] and side.waits[-1] is now[0]
+        hc.hc_adamw(plan, 1, stream=other)
+        assert {id(m) for m, _ in recorded} == {id(m) for m, _ in made} and all(s is other for _, s in recorded)
+    now[0].waits.clear()
+    hc.AdamWPlan.for_params(x, x)
+    assert made[-1][1] is now[0] and not now[0].waits
