@@ -318,12 +318,21 @@ __device__ __forceinline__ void lane_body(const Tensor& t, const Place& w, const
       fv[j] *= fv[j];
     }
   }
+  uint32_t least = ~0u;      // v that is not 0, and how it lies: v is not negative
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = fg[j] * n.c;
     fm[j] = n.b1 * fm[j] + n.a1 * x;
     fv[j] = n.b2 * fv[j] + n.a2 * (x * x);
     root[j] = BITS == 8 ? root_of(fv[j]) : __builtin_sqrtf(fv[j]);
+    if (BITS == 8) least = min(least, f32_bits(fv[j]) - 1);
+  }
+  if (BITS == 8 && least < f32_bits(kRootFrom) - 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) root[j] = any_root_of(fv[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
     const float den = __builtin_fmaf(root[j], n.unbias2, n.eps);
     fp[j] = __builtin_fmaf(-decay, fp[j], fp[j]);
     fp[j] = BITS == 8 ? __builtin_fmaf(-n.rate * fm[j], __builtin_amdgcn_rcpf(den), fp[j])

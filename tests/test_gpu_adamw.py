@@ -525,3 +525,48 @@ def test_plans_made_and_dropped_while_streams_are_busy():
         torch.cuda.synchronize()
         del junk
         assert torch.equal(got, want), (made, run)
+
+
+@pytest.mark.parametrize("seed", [0, 77])
+def test_roots_of_the_smallest_second_moments(seed):
+    """Gradients whose squares are among fp32's smallest numbers, zeroes and
+    ordinary ones between them: codes and scales by single operations, and the
+    step as with states of 32 bits."""
+    import numpy as np
+
+    f = np.float32
+    n = 40_000
+    rng = np.random.RandomState(3)
+    size = np.repeat(10.0 ** rng.uniform(-23.5, -14, n // 125), 125)       # blocks that two sizes share, too
+    size[::17] *= 1e-3
+    g = (rng.standard_normal(n) * size).astype(f)
+    g[::11] = 0
+    g[5000:5200] = 1e-3
+    p = torch.zeros(n, device="cuda")
+    other = p.clone()
+    grad = torch.from_numpy(g).cuda()
+    plan = hc.AdamWPlan.for_params([p], [grad], state_bits=8)
+    k = dict(lr=1e-3, betas=(0.9, 0.99), weight_decay=0.0, eps=1e-30)
+    hc.hc_adamw(plan, 1, seed=seed, **k)
+    hc.hc_adamw(hc.AdamWPlan.for_params([other], [grad]), 1, seed=seed, **k)
+    v = f(1 - 0.99) * (g * g)
+    root = np.sqrt(v)
+    assert ((v > 0) & (v < f(2.0 ** -126))).sum() > 5000
+    at = np.arange(n) // BLOCK
+    pad = np.zeros(-(-n // BLOCK) * BLOCK, f)
+    pad[:n] = root
+    unit = pad.reshape(-1, BLOCK).max(1) * f(f(1) / f(448))
+    off = plan.v_scales[0].cpu().numpy() != unit
+    assert not off.any(), int(off.sum())
+    y = np.divide(root, unit[at], out=np.zeros(n, f), where=unit[at] > 0)
+    if seed:
+        u = ((random_bits(seed, 1, 0, n).numpy() >> 16) + 0.5) / 65536
+        a = y.astype(np.float64)
+        step = np.exp2(np.clip(np.frexp(a)[1] - 1, -6, None) - 3.0)
+        y = np.minimum(np.floor(a / step + u) * step, 448)
+    y = torch.from_numpy(np.asarray(np.minimum(y, 448), f)).to(E4M3).float().numpy()
+    y = np.where((root > 0) & (y == 0), f(2.0 ** -9), y)
+    off = plan.exp_avg_sqs[0].cpu().float().numpy() != y
+    assert not off.any(), int(off.sum())
+    # the same m and root on both sides, a product, reciprocal and quotient apart: 8 U
+    close(p, other, other.abs() * 8 * U + TINY[F], "step")
