@@ -146,6 +146,15 @@ __device__ __forceinline__ float inverse(const Norm& n, float squares, Again aga
   return past ? 0x1p-80f * inverse_root(small + n.eps * 0x1p-80f * 0x1p-80f) : r;
 }
 
+// The scale of a group of 8 bits, peak * r / 448: the quotient of the factor that
+// keeps all of its bits so.  A row of zeroes without an eps has an infinite r.
+__device__ __forceinline__ float scale_of(float peak, float r) {
+  constexpr float k = 1.0f / 448.0f;
+  if (!(peak < __builtin_inff())) return __builtin_nanf("");
+  if (peak == 0.0f && r == r) return 0.0f;
+  return r < 0x1p-64f ? peak * k * r : peak * (r * k);
+}
+
 // N e4m3 codes, nearest.
 template <int N, bool NT>
 __device__ __forceinline__ void store_codes(uint8_t* p, const float* f, uint32_t skip) {
@@ -278,15 +287,15 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       float h[N], w[N];
       if (n.sum) store_vec<T, NT>(elem<T>(n.sum, t * n.sstride + at[u]), v[u]);
       if constexpr (Q8) {
-        // a group of tiny values is brought up first, so that 448 / a stays finite
-        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : 1.0f, a = peak[u] * lift;
+        // a group of tiny values is brought up first, so that 448 / a stays finite,
+        // and one of the largest down, whose reciprocal would be subnormal
+        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : peak[u] > 0x1p64f ? 0x1p-64f : 1.0f, a = peak[u] * lift;
         const float inv = peak[u] > 0.0f ? quotient(448.0f, a, reciprocal(a)) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) h[i] = prod[u][i] * lift * inv;
         store_codes<N, NT>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
         const uint32_t c = at[u] + skip[u];
-        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] =
-              peak[u] < __builtin_inff() ? peak[u] * (r * (1.0f / 448.0f)) : __builtin_nanf("");
+        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = scale_of(peak[u], r);
       } else {
         T::unpack(v[u], h);
         load_weight<T>(n, at[u], w);

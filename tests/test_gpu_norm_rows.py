@@ -373,3 +373,36 @@ def test_captured_and_on_a_stream(q8):
         got = [o.clone() for o in outs]
         step()
         assert all(torch.equal(raw(a), raw(b)) for a, b in zip(got, outs)), i
+
+
+def test_8_bits_at_the_end_of_the_range():
+    """Groups whose largest product lies within 2^4 of fp32's end, rows whose root
+    mean square does, and a row of zeroes with an eps of 0."""
+    g = gen(13)
+    d = 384
+    for dtype in (F, B):
+        for e, we in ((126, 0), (124, 2), (60, 66), (117, 0), (121, 0), (100, 25), (100, -90), (-60, -62)):
+            x = (torch.rand((5, d), generator=g, device="cuda") * 1.9 + 0.05).mul_(2.0 ** e).to(dtype)
+            w = torch.ones(d, device="cuda").mul_(2.0 ** we)
+            x[1, 128:256] *= 2.0 ** -20                       # a group of smaller values beside the others
+            x[2] *= -1
+            q, s = torch.empty((5, d), dtype=E4M3, device="cuda"), torch.empty((5, 3), device="cuda")
+            hc.hc_rms_norm_8bit(x, w, q, s, group=128, eps=0.0)
+            _, _, r, _ = norm64(x, None, w, 0.0)
+            prod = (x.float() * w).cpu().view(5, 3, 128)
+            a = prod.abs().amax(2, keepdim=True)
+            # 448 / a of a below 2^-119 is past fp32: both 2^64 times as large
+            up = torch.where(a < 2.0 ** -64, 2.0 ** 64, 1.0)
+            codes = (prod * up * (torch.full_like(a, 448.0) / (a * up))).view(5, d).to(E4M3).float()
+            assert bool((q.cpu().float() == codes).all()), (dtype, e, we)
+            # r below 2^-126 is off by half a step of the smallest numbers more
+            want = a[..., 0].double() * r / 448.0
+            close(s, want, want * (R + 3 * U + 2.0 ** -150 / r) + TINY[F], (dtype, e, we))
+        for d0 in (3, 300, 4096, 20001):
+            n = -(-d0 // 128)
+            x, w = torch.zeros((2, d0), device="cuda").to(dtype), torch.ones(d0, device="cuda")
+            q = torch.full((2, d0), 0x55, dtype=torch.uint8, device="cuda")
+            for group in (0, 128):
+                s = torch.full((2, n if group else 1), GUARD, device="cuda")
+                hc.hc_rms_norm_8bit(x, w, q, s, group=group, eps=0.0)
+                assert bool((s == 0).all()) and bool((q & 0x7F == 0).all()), (dtype, d0, group)
