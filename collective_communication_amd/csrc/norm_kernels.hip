@@ -111,20 +111,21 @@ template <uint32_t LPR, typename A, typename B>
 __device__ __forceinline__ void join_row(float& a, float& b, float* lds) {
   a = join_lanes<(LPR < 64 ? LPR : 64)>(a, A{});
   b = join_lanes<(LPR < 64 ? LPR : 64)>(b, B{});
-  if constexpr (LPR > 64) {
-    constexpr uint32_t W = LPR / 64, ALL = threads_of<LPR>() / 64;
-    const uint32_t wave = threadIdx.x >> 6, from = wave / W * W;
+  if constexpr (LPR > 64) {      // the workgroup's one row
+    static_assert(LPR == threads_of<LPR>(), "a row of several waves is a workgroup's");
+    constexpr uint32_t W = LPR / 64;
+    const uint32_t wave = threadIdx.x >> 6;
     if (lane_id() == 0) {
       lds[wave] = a;
-      lds[ALL + wave] = b;
+      lds[W + wave] = b;
     }
     __syncthreads();
-    a = lds[from];
-    b = lds[ALL + from];
+    a = lds[0];
+    b = lds[W];
 #pragma unroll
     for (uint32_t w = 1; w < W; ++w) {
-      a = A{}(a, lds[from + w]);
-      b = B{}(b, lds[ALL + from + w]);
+      a = A{}(a, lds[w]);
+      b = B{}(b, lds[W + w]);
     }
   }
 }
@@ -140,8 +141,7 @@ template <uint32_t LPR, typename Again>
 __device__ __forceinline__ float inverse(const Norm& n, float squares, Again again) {
   const bool past = squares == __builtin_inff();
   const float r = inverse_root((past ? squares : quotient(squares, n.width, n.per_width)) + n.eps);
-  // a workgroup of several rows goes through the barrier together
-  if (!(LPR == threads_of<LPR>() ? past : LPR > 64 ? (bool)__syncthreads_or(past) : (bool)__any(past))) return r;
+  if (!(LPR >= 64 ? past : (bool)__any(past))) return r;      // a wave's rows go together
   const float small = again() * n.per_width;      // an infinity's stay one
   return past ? 0x1p-80f * inverse_root(small + n.eps * 0x1p-80f * 0x1p-80f) : r;
 }
@@ -210,7 +210,7 @@ template <typename T, uint32_t LPR, int U, bool Q8, bool NT>
 __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
   constexpr int N = T::kVec;
   constexpr uint32_t RPW = threads_of<LPR>() / LPR;
-  __shared__ float lds[2][LPR > 64 ? 2 * threads_of<LPR>() / 64 : 1];
+  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
   const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   uint32_t turn = 0;
   for (size_t first = (size_t)blockIdx.x * RPW; first < n.ntokens; first += (size_t)gridDim.x * RPW) {
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
   constexpr int N = T::kVec;
   constexpr uint32_t RPW = threads_of<LPR>() / LPR;
   constexpr bool kAhead = U * N <= 16 && LPR < 1024;
-  __shared__ float lds[2][LPR > 64 ? 2 * threads_of<LPR>() / 64 : 1];
+  __shared__ float lds[2][LPR > 64 ? 2 * LPR / 64 : 1];
   __shared__ float tile[RPW > 1 ? threads_of<LPR>() * U * N : 1];
   const uint32_t slot = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   uint32_t turn = 0, at[U], skip[U];
