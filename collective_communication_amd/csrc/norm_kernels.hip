@@ -135,24 +135,26 @@ __device__ __forceinline__ float inverse_root(float x) {
   const bool small = x < 0x1p-100f;
   return __builtin_amdgcn_rsqf(small ? x * 0x1p64f : x) * (small ? 0x1p32f : 1.0f);
 }
-// 1 / sqrt(mean of squares + eps).  Where the squares pass what fp32 holds they
-// are summed once more, of values 2^80 smaller: again() does.
-template <uint32_t LPR, typename Again>
-__device__ __forceinline__ float inverse(const Norm& n, float squares, Again again) {
-  const bool past = squares == __builtin_inff();
-  const float r = inverse_root((past ? squares : quotient(squares, n.width, n.per_width)) + n.eps);
-  if (!(LPR >= 64 ? past : (bool)__any(past))) return r;      // a wave's rows go together
-  const float small = again() * n.per_width;      // an infinity's stay one
-  return past ? 0x1p-80f * inverse_root(small + n.eps * 0x1p-80f * 0x1p-80f) : r;
+// Whether it holds for one of a wave's rows (a row of several waves: in all of them).
+template <uint32_t LPR>
+__device__ __forceinline__ bool any_row(bool b) {
+  return LPR >= 64 ? b : (bool)__any(b);
 }
-
-// The scale of a group of 8 bits, peak * r / 448: the quotient of the factor that
-// keeps all of its bits so.  A row of zeroes without an eps has an infinite r.
-__device__ __forceinline__ float scale_of(float peak, float r) {
-  constexpr float k = 1.0f / 448.0f;
-  if (!(peak < __builtin_inff())) return __builtin_nanf("");
-  if (peak == 0.0f && r == r) return 0.0f;
-  return r < 0x1p-64f ? peak * k * r : peak * (r * k);
+// A row whose squares pass what fp32 holds is summed once more, of values f times
+// as large.
+// (x - x is 0 for what is finite, which takes no constant's register: past 96
+// scalar ones a SIMD holds 7 of the kernel's waves and not 8, and 60,000 x 2048
+// bf16 to 8 bits take 106 us and not 97.)
+__device__ __forceinline__ bool finite(float x) { return x - x == 0.0f; }
+__device__ __forceinline__ bool off_fp32(const Norm&, float squares) { return !finite(squares); }
+__device__ __forceinline__ float factor_of(bool off, float) {
+  return off ? 0x1p-80f : 1.0f;
+}
+// 1 / sqrt(mean of squares + eps) / f for the squares of f times the values: an
+// infinity's is 0.
+__device__ __forceinline__ float inverse(const Norm& n, float squares, float f) {
+  const float mean = f == 1.0f || finite(squares) ? quotient(squares, n.width, n.per_width) : squares;
+  return inverse_root(mean + n.eps * f * f);
 }
 
 // N e4m3 codes, nearest.
@@ -189,8 +191,10 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* f, uint32_t
   }
 }
 
+// By the steps of the first sum, so that a row beside one that needs this keeps
+// its bits.
 template <typename T, int U>
-__device__ __forceinline__ float small_squares(const typename T::vec* v, const uint32_t* skip) {
+__device__ __forceinline__ float squares_of(const typename T::vec* v, const uint32_t* skip, float f) {
   float sum = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -198,8 +202,8 @@ __device__ __forceinline__ float small_squares(const typename T::vec* v, const u
     T::unpack(v[u], h);
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) {
-      const float x = h[i] * 0x1p-80f;
-      sum += (uint32_t)i >= skip[u] ? x * x : 0.0f;
+      const float x = h[i] * f, s = __builtin_fmaf(x, x, sum);
+      sum = (uint32_t)i >= skip[u] ? s : sum;
     }
   }
   return sum;
@@ -269,12 +273,19 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
     }
     join_row<LPR, SumOp, MaxBits>(squares, top, lds[turn]);
     turn ^= 1;
-    const float r = inverse<LPR>(n, squares, [&] {
-      float sum = small_squares<T, U>(v, skip), none = 0.0f;
-      join_row<LPR, SumOp, SumOp>(sum, none, lds[turn]);
+    float r = inverse(n, squares, 1.0f);
+    // a group's scale is its largest by these two; of zeroes without an eps r is infinite
+    float ks[2] = {1.0f, squares == 0.0f ? 0.0f : r * (1.0f / 448.0f)};
+    if (const bool off = off_fp32(n, squares); __builtin_expect(any_row<LPR>(off), 0)) {
+      const float f = factor_of(off, squares);
+      float none = 0.0f;
+      squares = squares_of<T, U>(v, skip, f);
+      join_row<LPR, SumOp, SumOp>(squares, none, lds[turn]);
       turn ^= 1;
-      return sum;
-    });
+      r = f * inverse(n, squares, f);
+      ks[0] = f < 1.0f ? 1.0f / 448.0f : 1.0f;      // r / 448 may be subnormal
+      ks[1] = squares == 0.0f ? 0.0f : f < 1.0f ? r : r * (1.0f / 448.0f);
+    }
     if constexpr (Q8) {
       const uint32_t lanes = min(n.group / N, min(LPR, 64u));
 #pragma unroll
@@ -289,13 +300,20 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       if constexpr (Q8) {
         // a group of tiny values is brought up first, so that 448 / a stays finite,
         // and one of the largest down, whose reciprocal would be subnormal
-        const float lift = peak[u] < 0x1p-64f ? 0x1p64f : peak[u] > 0x1p64f ? 0x1p-64f : 1.0f, a = peak[u] * lift;
-        const float inv = peak[u] > 0.0f ? quotient(448.0f, a, reciprocal(a)) : 0.0f;
+        float a = peak[u];
+        if (__builtin_expect(__any((f32_bits(a) - f32_bits(0x1p-64f)) >> 30), 0)) {
+          const float lift = a > 1.0f ? 0x1p-64f : 0x1p64f;
+          a *= lift;
 #pragma unroll
-        for (int i = 0; i < N; ++i) h[i] = prod[u][i] * lift * inv;
+          for (int i = 0; i < N; ++i) prod[u][i] *= lift;
+        }
+        const float inv = a > 0.0f ? quotient(448.0f, a, reciprocal(a)) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = prod[u][i] * inv;
         store_codes<N, NT>(static_cast<uint8_t*>(n.out) + t * n.ostride + at[u], h, skip[u]);
         const uint32_t c = at[u] + skip[u];
-        if (c % n.group == 0) n.scales[t * n.cstride + c / n.group] = scale_of(peak[u], r);
+        if (c % n.group == 0)
+          n.scales[t * n.cstride + c / n.group] = peak[u] * ks[0] * ks[1] + (peak[u] - peak[u]);      // no number for none
       } else {
         T::unpack(v[u], h);
         load_weight<T>(n, at[u], w);
@@ -355,32 +373,36 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
     const bool there = t < n.ntokens, more = first + step < n.ntokens;
     if constexpr (kAhead)
       if (more) load(first + step, next);
-    float squares = 0.0f, dot = 0.0f;
+    float squares, dot, f = 1.0f;
+    auto sums = [&] {      // of h by f
+      squares = dot = 0.0f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (skip[u] == N) continue;
-      float h[N], dy[N], w[N];
-      T::unpack(row.v[u], h);
-      T::unpack(row.d[u], dy);
-      if constexpr (!kAhead) load_weight<T>(n, at[u], w);
+      for (int u = 0; u < U; ++u) {
+        if (skip[u] == N) continue;
+        float h[N], dy[N], w[N];
+        T::unpack(row.v[u], h);
+        T::unpack(row.d[u], dy);
+        if constexpr (!kAhead) load_weight<T>(n, at[u], w);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (kAhead) w[i] = wk[u][i];
-        const float a = __builtin_fmaf(h[i], h[i], squares), b = __builtin_fmaf(dy[i] * w[i], h[i], dot);
-        squares = (uint32_t)i >= skip[u] ? a : squares;
-        dot = (uint32_t)i >= skip[u] ? b : dot;
+        for (int i = 0; i < N; ++i) {
+          if constexpr (kAhead) w[i] = wk[u][i];
+          const float x = h[i] * f, a = __builtin_fmaf(x, x, squares), b = __builtin_fmaf(dy[i] * w[i], x, dot);
+          squares = (uint32_t)i >= skip[u] ? a : squares;
+          dot = (uint32_t)i >= skip[u] ? b : dot;
+        }
       }
-    }
-    join_row<LPR, SumOp, SumOp>(squares, dot, lds[turn]);
-    turn ^= 1;
-    const float r = inverse<LPR>(n, squares, [&] {
-      float sum = small_squares<T, U>(row.v, skip), none = 0.0f;
-      join_row<LPR, SumOp, SumOp>(sum, none, lds[turn]);
+      join_row<LPR, SumOp, SumOp>(squares, dot, lds[turn]);
       turn ^= 1;
-      return sum;
-    });
+    };
+    sums();
+    if (const bool off = off_fp32(n, squares); any_row<LPR>(off)) {
+      f = factor_of(off, squares);
+      sums();
+    }
+    const float root = inverse(n, squares, f), r = f * root;
+    dot = dot * n.per_width * root;
     if (there) {
-      const float back = dot * n.per_width * r * r;
+      const float back = dot * r;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (skip[u] == N) continue;
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           if constexpr (kAhead) w[i] = wk[u][i];
-          dw[u][i] = __builtin_fmaf(dy[i] * r, h[i], dw[u][i]);
+          dw[u][i] = __builtin_fmaf(h[i] * r, dy[i], dw[u][i]);      // h r is near 1, however large the row
           o[i] = __builtin_fmaf(r, __builtin_fmaf(-back, h[i], dy[i] * w[i]), o[i]);
         }
         // a vector moved back stores its own elements only: the others' dsum

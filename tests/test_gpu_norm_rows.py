@@ -406,3 +406,26 @@ def test_8_bits_at_the_end_of_the_range():
                 s = torch.full((2, n if group else 1), GUARD, device="cuda")
                 hc.hc_rms_norm_8bit(x, w, q, s, group=group, eps=0.0)
                 assert bool((s == 0).all()) and bool((q & 0x7F == 0).all()), (dtype, d0, group)
+
+
+@pytest.mark.parametrize("d", [2, 20, 64, 300, 1000, 2560, 4096, 9001, 20001])
+@pytest.mark.parametrize("dtype", [F, B])
+def test_gradient_of_large_rows(d, dtype):
+    """Rows whose squares, and whose products with the gradient, pass what fp32
+    holds, beside others, in the same wave too."""
+    g = gen(d + 1)
+    for e in (62, 70, 100, 118, 124):
+        t = 7
+        h = (torch.rand((t, d), generator=g, device="cuda") + 0.5).mul_(2.0 ** e).to(dtype)
+        h[1::2] *= 2.0 ** -e
+        dy = (torch.rand((t, d), generator=g, device="cuda") + 0.5).to(dtype)
+        w = torch.rand(d, generator=g, device="cuda") + 0.5
+        dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
+        hc.hc_rms_norm_grad(dy, h, w, dx, dw, space(hc.hc_rms_norm_grad_workspace_bytes(t, d)), eps=1e-6)
+        want, size, wdw, wsize = grads64(dy, h, w, 1e-6, None)
+        # with the roundings of r and of the mean among the smallest numbers, and
+        # the latter's product with h and r
+        r = 1.0 / (h.double().cpu().square().mean(1, keepdim=True) + 1e-6).sqrt()
+        tol = size * (200 * U + 2.0 ** -149 / r) + h.double().cpu().abs() * r * 2.0 ** -149
+        close(dx, want, tol + want.abs() * HALF[dtype] + 4 * TINY[dtype], f"dx 2^{e}")
+        close(dw, wdw, wsize * (R + (t + 4) * U + 2.0 ** -150 / float(r.min())), f"dw 2^{e}")
