@@ -54,6 +54,7 @@ struct Norm {
   uint32_t dim, group, groups;   // group: columns, the row's width or more for one
   uint32_t wbf16;
   float eps, width, per_width;   // the row's width and 1 / it
+  float least;                   // squares below it are summed again, larger
 };
 
 template <uint32_t LPR>
@@ -140,15 +141,17 @@ template <uint32_t LPR>
 __device__ __forceinline__ bool any_row(bool b) {
   return LPR >= 64 ? b : (bool)__any(b);
 }
-// A row whose squares pass what fp32 holds is summed once more, of values f times
-// as large.
+// A row whose squares pass what fp32 holds, or fall below what it holds beside an
+// eps as small, is summed once more, of values f times as large: below 2^-80 the
+// squares that are lost count (32,768 of 2^-149), and 2^96 brings the smallest
+// square up to 2^-106 and the sums not past 2^112.
 // (x - x is 0 for what is finite, which takes no constant's register: past 96
 // scalar ones a SIMD holds 7 of the kernel's waves and not 8, and 60,000 x 2048
 // bf16 to 8 bits take 106 us and not 97.)
 __device__ __forceinline__ bool finite(float x) { return x - x == 0.0f; }
-__device__ __forceinline__ bool off_fp32(const Norm&, float squares) { return !finite(squares); }
-__device__ __forceinline__ float factor_of(bool off, float) {
-  return off ? 0x1p-80f : 1.0f;
+__device__ __forceinline__ bool off_fp32(const Norm& n, float squares) { return !finite(squares) || squares < n.least; }
+__device__ __forceinline__ float factor_of(bool off, float squares) {
+  return !off ? 1.0f : squares > 1.0f ? 0x1p-80f : 0x1p96f;
 }
 // 1 / sqrt(mean of squares + eps) / f for the squares of f times the values: an
 // infinity's is 0.
@@ -274,8 +277,7 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
     join_row<LPR, SumOp, MaxBits>(squares, top, lds[turn]);
     turn ^= 1;
     float r = inverse(n, squares, 1.0f);
-    // a group's scale is its largest by these two; of zeroes without an eps r is infinite
-    float ks[2] = {1.0f, squares == 0.0f ? 0.0f : r * (1.0f / 448.0f)};
+    float ks[2] = {1.0f, r * (1.0f / 448.0f)};      // a group's scale is its largest by these two
     if (const bool off = off_fp32(n, squares); __builtin_expect(any_row<LPR>(off), 0)) {
       const float f = factor_of(off, squares);
       float none = 0.0f;
@@ -283,7 +285,8 @@ __global__ void __launch_bounds__(threads_of<LPR>()) norm_kernel(Norm n) {
       join_row<LPR, SumOp, SumOp>(squares, none, lds[turn]);
       turn ^= 1;
       r = f * inverse(n, squares, f);
-      ks[0] = f < 1.0f ? 1.0f / 448.0f : 1.0f;      // r / 448 may be subnormal
+      // of large rows r / 448 may be subnormal, and of one of zeroes without an eps r is infinite
+      ks[0] = f < 1.0f ? 1.0f / 448.0f : 1.0f;
       ks[1] = squares == 0.0f ? 0.0f : f < 1.0f ? r : r * (1.0f / 448.0f);
     }
     if constexpr (Q8) {
@@ -556,6 +559,7 @@ Norm norm_of(const NormRows& a) {
   n.eps = a.eps;
   n.width = (float)a.dim;
   n.per_width = 1.0f / n.width;
+  n.least = n.eps < 0x1p-80f ? 0x1p-80f : 0.0f;
   return n;
 }
 

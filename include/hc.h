@@ -695,7 +695,10 @@ hc_status_t hc_expert_combine_grad(const void *dout, hc_dtype_t dtype, size_t di
  *   out = round(h * r * weight),   r = 1 / sqrt(mean of h^2 + eps)
  * in fp32; h is rounded to the rows' type first, so that the norm and its
  * gradient are of the values that sum_out holds.  No finite row's squares
- * overflow.  A NaN makes its row NaN; an infinity makes the row 0 and itself NaN.
+ * overflow, nor do they vanish beside an eps of 0 or one as small (where r is
+ * past fp32, with a mean of squares and an eps below 2^-256 together, the row is
+ * infinite; of zeroes alone it is NaN).  A NaN makes its row NaN; an infinity
+ * makes the row 0 and itself NaN.
  *   x, residual, sum_out, out: ntokens rows of dtype, each with its stride; dim
  *     in 1..HC_MAX_NORM_DIM.
  *     residual may be NULL, and so may sum_out (h is then not kept); sum_out
@@ -733,7 +736,10 @@ hc_status_t hc_rms_norm_8bit(const void *x, hc_dtype_t dtype, size_t ntokens, si
  *   dx = round(r * (dout * weight - h * r^2 * mean(dout * weight * h)) + dsum)
  *   dweight = round(sum over tokens of dout * h * r), or with accumulate != 0
  *     round(dweight + that sum)
- * in fp32; the order of the sums follows the sizes.
+ * in fp32; the order of the sums follows the sizes.  dout * weight is fp32's, and
+ * so is its product with h, summed over a row, unless the row's squares pass
+ * fp32 themselves (then of h 2^-80 times as large).  A NaN or an infinity in h
+ * makes its row of dx NaN.
  *   dsum: the gradient that arrives at h beside the norm's, or NULL.  dx may
  *     be dout, h or dsum, with its stride.
  *   dweight: dim elements of dweight_dtype, or NULL (not computed).

@@ -429,3 +429,55 @@ def test_gradient_of_large_rows(d, dtype):
         tol = size * (200 * U + 2.0 ** -149 / r) + h.double().cpu().abs() * r * 2.0 ** -149
         close(dx, want, tol + want.abs() * HALF[dtype] + 4 * TINY[dtype], f"dx 2^{e}")
         close(dw, wdw, wsize * (R + (t + 4) * U + 2.0 ** -150 / float(r.min())), f"dw 2^{e}")
+
+
+@pytest.mark.parametrize("d", [2, 20, 64, 300, 1000, 2560, 4096, 9001, 20001])
+@pytest.mark.parametrize("dtype", [F, B])
+def test_tiny_rows_and_a_tiny_eps(d, dtype):
+    """Rows whose squares fall below fp32's smallest numbers, where eps is 0 or as
+    small as they are: the norm, its 8 bits' scales and the gradient."""
+    g = gen(d + 2)
+    for e, eps in ((-45, 0.0), (-62, 0.0), (-72, 0.0), (-72, 2.0 ** -142), (-100, 0.0), (-100, 2.0 ** -149), (-120, 0.0)):
+        t = 7
+        h = torch.randn((t, d), generator=g, device="cuda").mul_(2.0 ** e).to(dtype)
+        h[1::2] *= 2.0 ** -e
+        h[::2, 0] = 2.0 ** e                                    # no row of zeroes
+        w = torch.rand(d, generator=g, device="cuda") + 0.5
+        out = torch.empty_like(h)
+        hc.hc_rms_norm(h, w, out, eps=eps)
+        _, _, r, y = norm64(h, None, w, eps)
+        close(out, y, y.abs() * (R + 3 * U + HALF[dtype]) + TINY[dtype], f"2^{e}")
+        q, s = torch.empty((t, d), dtype=E4M3, device="cuda"), torch.empty((t, 1), device="cuda")
+        hc.hc_rms_norm_8bit(h, w, q, s, eps=eps)
+        want = (h.float() * w).abs().amax(1, keepdim=True).double().cpu() * r / 448
+        close(s, want, want * (R + 3 * U) + TINY[F], f"scales 2^{e}")
+        assert bool((q.float().abs().amax(1) == 448).all())
+        value = q.cpu().double() * s.cpu().double()
+        close(value, y, y.abs() * (2.0 ** -4 + R + 6 * U) + s.cpu().double() * 2.0 ** -10 * 1.01, f"8 bits 2^{e}")
+        dy = torch.randn((t, d), generator=g, device="cuda").mul_(2.0 ** -20).to(dtype)
+        dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
+        hc.hc_rms_norm_grad(dy, h, w, dx, dw, space(hc.hc_rms_norm_grad_workspace_bytes(t, d)), eps=eps)
+        want, size, wdw, wsize = grads64(dy, h, w, eps, None)
+        close(dx, want, size * 200 * U + want.abs() * HALF[dtype] + TINY[dtype], f"dx 2^{e}")
+        close(dw, wdw, wsize * (R + (t + 4) * U), f"dw 2^{e}")
+
+
+@pytest.mark.parametrize("d", [2, 20, 64, 120, 250, 500])
+@pytest.mark.parametrize("dtype", [F, B])
+def test_rows_beside_far_ones_keep_their_bits(d, dtype):
+    """Rows of one wave, some of which are summed twice: the others are as they
+    are alone."""
+    g = gen(d + 3)
+    x, dy, w = rows(g, 64, d, dtype), rows(g, 64, d, dtype), torch.rand(d, generator=g, device="cuda") + 0.5
+    far = x.clone()
+    far[1::4] *= 2.0 ** 100
+    far[2::4] *= 2.0 ** -100
+    out = []
+    for h in (x, far):
+        y, q = torch.empty_like(h), torch.empty((64, d), dtype=E4M3, device="cuda")
+        s, dx = torch.empty((64, -(-d // 32)), device="cuda"), torch.empty_like(h)
+        hc.hc_rms_norm(h, w, y, eps=0.0)
+        hc.hc_rms_norm_8bit(h, w, q, s, group=32, eps=0.0)
+        hc.hc_rms_norm_grad(dy, h, w, dx, eps=0.0)
+        out.append([v.view(16, 4, -1)[:, ::3] for v in (y, q.view(torch.uint8), s, dx)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
