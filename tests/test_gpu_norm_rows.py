@@ -481,3 +481,25 @@ def test_rows_beside_far_ones_keep_their_bits(d, dtype):
         hc.hc_rms_norm_grad(dy, h, w, dx, eps=0.0)
         out.append([v.view(16, 4, -1)[:, ::3] for v in (y, q.view(torch.uint8), s, dx)])
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("t,d,dtype", [(600, 2560, F), (2100, 4096, B), (700, 8195, B), (300, 20001, F), (300, 20001, B),
+                                       (1100, 6000, B), (1300, 520, F), (9000, 256, B)])
+def test_more_rows_than_workgroups(t, d, dtype):
+    """Every layout with more rows than workgroups: the weight's gradient over all
+    of a workgroup's rows, and dx onto what the next row's loads run ahead of."""
+    g = gen(t + d)
+    dy, h, ds = (rows(g, t, d, dtype) for _ in range(3))
+    w = torch.randn(d, generator=g, device="cuda")
+    dx, dw = torch.empty_like(dy), torch.empty(d, device="cuda")
+    ws = space(hc.hc_rms_norm_grad_workspace_bytes(t, d))
+    hc.hc_rms_norm_grad(dy, h, w, dx, dw, ws, dsum=ds)
+    want, size, wdw, wsize = grads64(dy, h, w, 1e-6, ds)
+    add = ds.double().cpu().abs() * 2 * U
+    close(dx, want, size * 200 * U + add + want.abs() * HALF[dtype] + TINY[dtype], "dx")
+    close(dw, wdw, wsize * (R + (t + 4) * U) + TINY[F], "dw")
+    for i in range(3):
+        v = [dy.clone(), h.clone(), ds.clone()]
+        again = torch.empty_like(dw)
+        hc.hc_rms_norm_grad(v[0], v[1], w, v[i], again, ws, dsum=v[2])
+        assert torch.equal(v[i], dx) and torch.equal(again, dw), i
