@@ -375,12 +375,17 @@ __global__ void __launch_bounds__(kThreads, LPT * V <= 512 ? 6 : 1) route_kernel
 #pragma unroll
   for (uint32_t v = 0; v < V; ++v) key[v] = (key[v] & ~(V - 1)) | (V - 1 - v);
   // How far a value's key may be from it: what the key cuts off and a sum's
-  // rounding, relative to it, and the score's own error.  An exponential of x is
-  // off by |x| + 2 halves of an ulp, and |x| s (1 - s) and |x| e^-|x| are below
-  // 0.4, so that a score, with its quotient and sum over the row, is off by
-  // 2^-20 of the largest that there can be.
-  constexpr float kCut = V * 0x1p-23f;
-  const float unit = 0x1p-20f * (softmax ? 1.0f / z : 1.0f);
+  // rounding, relative to it, and the score's own error, in halves of an ulp, 2^-24.
+  // An exponential of x is off by |x| + 2 of them, and (|x| + 2) e^-|x| is at most 2.
+  // A sigmoid: |x| s (1 - s) is below 0.3, and s (1 - s) at most 1/4, with the
+  // argument's constant, its sum and its quotient below 8; 16 are taken.
+  // A softmax, relative to the largest that there can be, 1 / z: the exponential 2
+  // and the product 1 for each of two that are compared, and for both together the
+  // reciprocal 2 and z, by V - 1 sums in turn, 6 over the lanes and its exponentials'
+  // 2 and mean |x|, which for 1024 experts is below 4.5: V + 20 for two, V / 2 + 10
+  // for one; V / 2 + 12 are taken, and 16 at least.
+  constexpr float kCut = V * 0x1p-23f, kSoft = V > 8 ? V / 2 + 12 : 16;
+  const float unit = softmax ? kSoft * 0x1p-24f / z : 0x1p-20f;
   auto off = [=](float c) { return fabsf(c) * (kCut + 0x1p-23f) + unit; };
   uint32_t top4[4];
   largest4<V>(key, top4);

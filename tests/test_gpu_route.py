@@ -370,3 +370,28 @@ def test_no_tokens():
     x = torch.empty((0, 16), device="cuda")
     hc.hc_route(x, torch.empty((0, 2), dtype=torch.int32, device="cuda"), torch.empty((0, 2), device="cuda"))
     hc.hc_route_grad(x, torch.empty((0, 2), dtype=torch.int32, device="cuda"), torch.empty((0, 2), device="cuda"), x)
+
+
+@pytest.mark.parametrize("lanes,base", [(31, -0.6919994354248047), (31, -0.6913518905639648), (32, -0.6879949569702148),
+                                        (33, -0.6879949569702148), (33, -0.692230224609375), (33, -0.6923713684082031)])
+def test_values_nearer_than_a_sums_rounding(lanes, base):
+    """Softmax scores with a bias, of which two differ by less than what the row's
+    sum in fp32 is off by: 31 experts a lane, an exponential just above 1/2 that is
+    rounded down, and thirty just below half a step of it, which the sum loses."""
+    groups, each = 33, 31
+    x = torch.full((groups, each), -17.33)
+    x[:, 0] = base
+    x[0, 0] = 0.0
+    x[lanes:] = NEVER
+    x = x.view(1, -1)
+    s = scores64(x.double(), "softmax")[0]
+    bias = torch.full((groups * each,), NEVER)
+    bias[0] = -s[0]
+    first = s[0] + bias[0].double()
+    # the second value above the first by so many times 2^-24 of the largest score
+    for more in (1e-5, 1e-3, 0.3, 1.0, 3.0, 10.0):
+        bias[1] = first - s[1] + more * U * s[0]
+        assert float(s[1] + bias[1].double()) > float(first)
+        for k, want in ((1, [1]), (2, [1, 0])):
+            e, _ = check(x.cuda(), k, bias=bias.cuda(), groups=groups, top_groups=groups, renormalise=False)
+            assert e.tolist() == [want]
