@@ -785,7 +785,8 @@ class AdamWPlan:
     and is known to every stream of torch's that a step runs on: a plan may be
     dropped while its steps are pending.  Where a step ran on another stream
     that is not torch's (a raw handle, an ExternalStream), which may be gone
-    before the plan is, the plan is kept until that step is done."""
+    before the plan is, the plan is kept until that step is done; and while a
+    captured step may be replayed."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_scales=None, copies=None, decays=None,
                  table: torch.Tensor | None = None, stream=None):

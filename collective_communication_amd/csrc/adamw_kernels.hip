@@ -16,14 +16,16 @@
 // 17 bits of range that e4m3 has below its block's largest.  A block is 16
 // lanes, whose largest magnitude four DPP steps find.  Their step is bound by
 // the lanes' work as much as by memory (some 60 instructions a value, the
-// random bits' three products, a root and two reciprocals among them), so roots,
-// reciprocals and quotients come from the 1-ulp instructions with one correction,
-// and the conversions round by random bits themselves.
+// random bits' three products, a root and two reciprocals among them), so what is
+// stored comes from the 1-ulp instructions with one correction (the parameter's
+// own quotient from the reciprocal as it is, 1 ulp), and the conversions round by
+// random bits themselves.
 //
-// Measured: 2^25 values of 290 views, fp32 states and gradients, mixed parameters
-// (808 MB) 148 us, 5.4 TB/s (a large copy: 4.8-5.2); 2^28 bf16 values of 450
-// tensors, 8 bits, random bits (2.72 GB) 570 us, 4.8 TB/s; 3 * 10^5 fp32 values of
-// 12 tensors 5.4 us.  Non-temporal loads and stores: 2^25 values 162 us, 2^28 566.
+// Measured in a loop: 2^25 values of 290 views, fp32 states and gradients, mixed
+// parameters (808 MB) 150 us, 5.4 TB/s (a large copy: 4.8-5.2); 2^28 bf16 values of
+// 450 tensors, 8 bits, random bits (2.72 GB) 536 us, 5.1 TB/s; 3 * 10^5 fp32 values
+// of 12 tensors 5.1 us.  By a trace of the kernels, as all variants here are: 149,
+// 571 and 5.4; non-temporal loads and stores 162 (2^25 values) and 566 (2^28).
 #include <math.h>
 
 #include "arith.hpp"
@@ -327,7 +329,7 @@ __device__ __forceinline__ void lane_body(const Tensor& t, const Place& w, const
     root[j] = BITS == 8 ? root_of(fv[j]) : __builtin_sqrtf(fv[j]);
     if (BITS == 8) least = min(least, f32_bits(fv[j]) - 1);
   }
-  if (BITS == 8 && least < f32_bits(kRootFrom) - 1) {
+  if (BITS == 8 && least < f32_bits(kRootFrom) - 1) {      // few lanes: 536 us of 2^28 values with and without
 #pragma unroll
     for (int j = 0; j < 8; ++j) root[j] = any_root_of(fv[j]);
   }

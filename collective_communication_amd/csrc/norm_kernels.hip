@@ -13,14 +13,14 @@
 // partials per workgroup, which a second launch adds in a fixed order.
 //
 // Measured (a large copy reaches 4.8-5.2 TB/s here): 16,384 x 4096 bf16 with a residual
-// to 8 bits, a scale for 128 columns (472 MB) 92 us, 5.1 TB/s (105 with plain
+// to 8 bits, a scale for 128 columns (472 MB) 93 us, 5.1 TB/s (105 with plain
 // stores and joins through shared memory, 111 by 8 waves a row, 126 by 2); 60,000 x
-// 2048 without a residual, which is bound by the lanes' work, 106 us (131 with full
+// 2048 without a residual, which is bound by the lanes' work, 103 us (131 with full
 // divisions and each product made twice).  Its gradient with dsum, 16,384 x
-// 4096 (537 MB) 92 us, 5.8 TB/s, and 7 for the weight's partials: 97 with these
-// stored by single values, 118 without the next row's loads ahead, or with them and
-// 130 registers instead of 128.  64 x 4096 to 8 bits 4.3 us, 500 x 2560 fp32
-// gradient 6.5 + 4.2.
+// 4096 (537 MB) 96 us, 5.6 TB/s, and 7.5 for the weight's partials: 118 without the
+// next row's loads ahead, or with them and 130 registers instead of 128.  64 x 4096
+// to 8 bits 4.4 us, 500 x 2560 fp32 gradient 6.7 + 4.1.  All by a trace of the
+// kernels; in a loop the calls take 91 and 101 us, and 97 for 60,000 x 2048.
 #include <type_traits>
 
 #include "arith.hpp"
@@ -376,8 +376,11 @@ __global__ void __launch_bounds__(threads_of<LPR>(), LPR >= 64 && LPR < 1024 && 
     const bool there = t < n.ntokens, more = first + step < n.ntokens;
     if constexpr (kAhead)
       if (more) load(first + step, next);
+    // Both sums, of h by f.  Written out twice, the first with f = 1: 16,384 x 4096
+    // bf16 take 117 us and not 101 where the second reads the weights again, 128 where
+    // a loop goes back with f (registers past 128 in either).
     float squares, dot, f = 1.0f;
-    auto sums = [&] {      // of h by f
+    auto sums = [&] {
       squares = dot = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
