@@ -527,11 +527,12 @@ def test_plans_made_and_dropped_while_streams_are_busy():
         assert torch.equal(got, want), (made, run)
 
 
+@pytest.mark.parametrize("eps", [1e-30, 0.0])
 @pytest.mark.parametrize("seed", [0, 77])
-def test_roots_of_the_smallest_second_moments(seed):
+def test_roots_of_the_smallest_second_moments(seed, eps):
     """Gradients whose squares are among fp32's smallest numbers, zeroes and
     ordinary ones between them: codes and scales by single operations, and the
-    step as with states of 32 bits."""
+    step as with states of 32 bits (without an eps no number where v is 0)."""
     import numpy as np
 
     f = np.float32
@@ -546,7 +547,7 @@ def test_roots_of_the_smallest_second_moments(seed):
     other = p.clone()
     grad = torch.from_numpy(g).cuda()
     plan = hc.AdamWPlan.for_params([p], [grad], state_bits=8)
-    k = dict(lr=1e-3, betas=(0.9, 0.99), weight_decay=0.0, eps=1e-30)
+    k = dict(lr=1e-3, betas=(0.9, 0.99), weight_decay=0.0, eps=eps)
     hc.hc_adamw(plan, 1, seed=seed, **k)
     hc.hc_adamw(hc.AdamWPlan.for_params([other], [grad]), 1, seed=seed, **k)
     v = f(1 - 0.99) * (g * g)
@@ -569,4 +570,4 @@ def test_roots_of_the_smallest_second_moments(seed):
     off = plan.exp_avg_sqs[0].cpu().float().numpy() != y
     assert not off.any(), int(off.sum())
     # the same m and root on both sides, a product, reciprocal and quotient apart: 8 U
-    close(p, other, other.abs() * 8 * U + TINY[F], "step")
+    close(p, other, torch.where(other.isfinite(), other.abs() * 8 * U, 0.0) + TINY[F], "step")
